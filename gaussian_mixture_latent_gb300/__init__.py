@@ -22,7 +22,8 @@ __all__ = [
     "gma_forward_ex", "gma_forward_plan", "gma_forward_call", "gma_forward_multi",
     "gma_responsibilities", "gma_diagnostics", "gma_forward_cross", "gma_decode", "gma_backward",
     "gma_proj_desc", "gma_project", "gma_selftest_timeout", "gma_get_status", "gma_status_string", "gma_version",
-    "Workspace", "library_path",
+    "Workspace", "library_path", "gma_delta_desc", "gma_delta_forward", "gma_delta_backward", "gma_delta_decode",
+    "gma_state_desc", "gma_state_store", "gma_state_load",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -550,10 +551,17 @@ def gma_selftest_timeout(workspace, stream=None):
 
 
 def gma_get_status(workspace=None, stream=None) -> int:
-    """Synchronise, read and clear the device status word; returns the gma_status code."""
-    if workspace is None:
-        key = torch.cuda.current_device()
-        if key not in _default_ws or _default_ws[key].buf is None:
-            return 0
-        workspace = _default_ws[key].buf
-    return _load().gma_get_status(_ptr(workspace), _stream_ptr(stream))
+    """Synchronise, read and clear the device status word; returns the gma_status code.
+    Without `workspace`: those of this module's own buffers for the current device and `stream`."""
+    if workspace is not None:
+        return _load().gma_get_status(_ptr(workspace), _stream_ptr(stream))
+    key = torch.cuda.current_device()
+    own = [_default_ws[key].buf] if key in _default_ws else []
+    own.append(_delta_scratch.get((key, _stream_ptr(stream))))
+    codes = [_load().gma_get_status(_ptr(ws), _stream_ptr(stream)) for ws in own if ws is not None]
+    return next((c for c in codes if c), 0)
+
+
+from .delta import _scratch as _delta_scratch  # noqa: E402
+from .delta import (gma_delta_backward, gma_delta_decode, gma_delta_desc, gma_delta_forward,  # noqa: E402
+                    gma_state_desc, gma_state_load, gma_state_store)

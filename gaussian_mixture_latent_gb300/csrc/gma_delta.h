@@ -1,0 +1,80 @@
+// Internal declarations of the gated delta rule and the quantised state cache.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "gma_internal.h"
+
+namespace gma {
+
+// Per value head h of batch entry b (key head h / (H / Hk)), with the state S [d, dv] in fp32:
+//   w_t = v_t - e^{g_t} S_{t-1}^T k_t,   S_t = e^{g_t} S_{t-1} + k_t (beta_t w_t)^T,   o_t = scale S_t^T q_t.
+struct DeltaProblem {
+    int B, H, Hk, N, d, dv;
+    bool bf16, gate_bf16;             // types of Qx, Kx, V, out and of g, beta
+    float scale;
+    const void *Qx, *Kx, *V, *g, *beta;
+    const int *lengths;               // [B] or null: rows at and past the length do not exist
+    unsigned *status;
+};
+
+// ----- one row after another, fp32 on the CUDA cores, any shape: gma_delta_rec.cu -----
+constexpr int kRecChunk = 32;         // rows between two checkpoints of the row-by-row backward
+struct DeltaRec {
+    const float *state_in;            // [pool, H, d, dv] or null (zeros)
+    float *state_out;                 // the same layout, or null; may equal state_in
+    const int *slots;                 // [B] pool index of each batch entry, or null (entry b at b)
+    int n_states;
+    void *out;                        // forward: O; backward: dV (types of V)
+    float *rows_out;                  // forward: w [G, N, dv]; backward: dU [G, N, dv]; or null
+    float *ckpt;                      // [G, ceil(N / kRecChunk), d, dv]: S before / dS after each chunk; or null
+};
+cudaError_t delta_rec_forward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s);
+// p.V is dO; state_in is dL/dS after the last row, state_out dL/dS before the first
+cudaError_t delta_rec_backward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s);
+
+struct DeltaGrads {
+    const void *dO;
+    const float *w, *du;              // [G, N, dv]
+    const float *s0, *ds;             // checkpoints of the two recurrences
+    float *dq_heads, *dk_heads;       // [G, N, d] per value head; null when H == Hk
+    void *dQ, *dK, *dg, *dbeta;
+};
+cudaError_t delta_rec_grads(const DeltaProblem &p, const DeltaGrads &a, cudaStream_t s);
+// dQ, dK as the sums of the H / Hk value heads of each key head (in order)
+cudaError_t delta_sum_heads(const DeltaProblem &p, const float *dq_heads, const float *dk_heads, void *dQ, void *dK,
+                            cudaStream_t s);
+
+// ----- 8-bit state cache: gma_state.cu -----
+struct StateCopy {
+    int n, n_states, n_cache;
+    long long rows;                   // rows of one state
+    int cols;
+    const int *src, *dst;             // [n] or null (entry i at i)
+    unsigned *status;
+};
+cudaError_t state_store(const StateCopy &p, const float *state, signed char *codes, float *scales, cudaStream_t s);
+cudaError_t state_load(const StateCopy &p, const signed char *codes, const float *scales, float *state,
+                       cudaStream_t s);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float delta_in(const float *p, size_t i) { return p[i]; }
+__device__ __forceinline__ float delta_in(const __nv_bfloat16 *p, size_t i) { return __bfloat162float(p[i]); }
+__device__ __forceinline__ void delta_out(float *p, size_t i, float v) { p[i] = v; }
+__device__ __forceinline__ void delta_out(__nv_bfloat16 *p, size_t i, float v) { p[i] = __float2bfloat16_rn(v); }
+__device__ __forceinline__ float delta_gate(const void *p, size_t i, bool bf16) {
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];
+}
+__device__ __forceinline__ void delta_gate_out(void *p, size_t i, float v, bool bf16) {
+    if (bf16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+    else static_cast<float *>(p)[i] = v;
+}
+__device__ __forceinline__ int delta_len(const int *lengths, int b, int N) {
+    return lengths ? min(max(lengths[b], 0), N) : N;
+}
+// A log decay at or below -1e5 forgets everything (e^g = 0 in fp32); holding it there keeps sums of a chunk's
+// decays finite, so that minus infinity and the type's lowest value are ordinary inputs.  NaN passes through.
+__device__ __forceinline__ float delta_floor(float g) { return g < -1e5f ? -1e5f : g; }
+#endif
+
+}  // namespace gma

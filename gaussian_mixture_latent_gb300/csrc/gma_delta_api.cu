@@ -1,0 +1,220 @@
+// Host side of the gated delta rule and of the quantised state cache (include/gma.h): argument checks, workspace
+// carving and launches.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "gma_delta.h"
+
+namespace gma {
+namespace {
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+gma_status validate(const gma_delta_desc *d) {
+    if (!d) return GMA_ERR_INVALID_ARG;
+    if (d->B <= 0 || d->H <= 0 || d->Hk <= 0 || d->H % d->Hk != 0 || d->N < 0) return GMA_ERR_INVALID_ARG;
+    if (d->d <= 0 || d->dv <= 0) return GMA_ERR_INVALID_ARG;
+    if (d->in_dtype != GMA_F32 && d->in_dtype != GMA_BF16) return GMA_ERR_INVALID_ARG;
+    if (d->gate_dtype != GMA_F32 && d->gate_dtype != GMA_BF16) return GMA_ERR_INVALID_ARG;
+    if (!std::isfinite(d->scale)) return GMA_ERR_INVALID_ARG;
+    if (d->d > 256 || d->dv > 256) return GMA_ERR_UNSUPPORTED;
+    if ((long long)d->B * d->H > 65535 || (long long)d->B * d->H * d->N > (1LL << 31)) return GMA_ERR_UNSUPPORTED;
+    return GMA_OK;
+}
+
+DeltaProblem problem(const gma_delta_desc *d, const void *Qx, const void *Kx, const void *V, const void *g,
+                     const void *beta, const int *lengths, void *ws) {
+    DeltaProblem p{};
+    p.B = d->B; p.H = d->H; p.Hk = d->Hk; p.N = d->N; p.d = d->d; p.dv = d->dv;
+    p.bf16 = d->in_dtype == GMA_BF16;
+    p.gate_bf16 = d->gate_dtype == GMA_BF16;
+    p.scale = d->scale;
+    p.Qx = Qx; p.Kx = Kx; p.V = V; p.g = g; p.beta = beta; p.lengths = lengths;
+    p.status = static_cast<unsigned *>(ws);
+    return p;
+}
+
+template <int M>
+bool all_aligned(const void *const (&ptrs)[M]) {
+    for (const void *q : ptrs)
+        if (q && !aligned16(q)) return false;
+    return true;
+}
+
+gma_status launched(cudaError_t e) { return e == cudaSuccess ? GMA_OK : GMA_ERR_CUDA; }
+
+struct BwdLayout2 {
+    size_t w, du, s0, ds, dq, dk, total;
+};
+
+BwdLayout2 backward_layout(const gma_delta_desc *d) {
+    const size_t G = (size_t)d->B * d->H, rows = G * d->N;
+    const size_t nchunk = ((size_t)d->N + kRecChunk - 1) / kRecChunk;
+    BwdLayout2 L{};
+    size_t o = kHeaderBytes;
+    auto take = [&](size_t floats) { const size_t at = o; o += align_up(floats * sizeof(float)); return at; };
+    L.w = take(rows * d->dv);
+    L.du = take(rows * d->dv);
+    L.s0 = take(G * nchunk * d->d * d->dv);
+    L.ds = take(G * nchunk * d->d * d->dv);
+    if (d->H != d->Hk) {
+        L.dq = take(rows * d->d);
+        L.dk = take(rows * d->d);
+    }
+    L.total = o;
+    return L;
+}
+
+}  // namespace
+}  // namespace gma
+
+using namespace gma;
+
+extern "C" {
+
+gma_status gma_delta_workspace_size(const gma_delta_desc *desc, size_t *bytes) {
+    const gma_status st = validate(desc);
+    if (st != GMA_OK) return st;
+    if (!bytes) return GMA_ERR_INVALID_ARG;
+    *bytes = kHeaderBytes;
+    return GMA_OK;
+}
+
+gma_status gma_delta_forward(const gma_delta_desc *desc, const void *Qx, const void *Kx, const void *V, const void *g,
+                             const void *beta, const int *lengths, const float *state_in, void *out, float *state_out,
+                             void *workspace, size_t workspace_bytes, void *stream) {
+    size_t need = 0;
+    const gma_status st = gma_delta_workspace_size(desc, &need);
+    if (st != GMA_OK) return st;
+    if (desc->N > 0 && (!Qx || !Kx || !V || !g || !beta || !out)) return GMA_ERR_INVALID_ARG;
+    const void *const ptrs[] = {Qx, Kx, V, g, beta, lengths, state_in, out, state_out, workspace};
+    if (!all_aligned(ptrs)) return GMA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < need) return GMA_ERR_WORKSPACE;
+    if (desc->N == 0 && (!state_out || state_out == state_in)) return GMA_OK;
+    const DeltaProblem p = problem(desc, Qx, Kx, V, g, beta, lengths, workspace);
+    DeltaRec r{};
+    r.state_in = state_in;
+    r.state_out = state_out;
+    r.out = out;
+    return launched(delta_rec_forward(p, r, static_cast<cudaStream_t>(stream)));
+}
+
+gma_status gma_delta_decode_workspace_size(const gma_delta_desc *desc, size_t *bytes) {
+    const gma_status st = validate(desc);
+    if (st != GMA_OK) return st;
+    if (!bytes) return GMA_ERR_INVALID_ARG;
+    *bytes = kHeaderBytes;
+    return GMA_OK;
+}
+
+gma_status gma_delta_decode(const gma_delta_desc *desc, const void *Qx, const void *Kx, const void *V, const void *g,
+                            const void *beta, const int *lengths, const int *slots, int n_states, float *state,
+                            void *out, void *workspace, size_t workspace_bytes, void *stream) {
+    const gma_status st = validate(desc);
+    if (st != GMA_OK) return st;
+    if (!state || n_states <= 0 || (!slots && n_states < desc->B)) return GMA_ERR_INVALID_ARG;
+    if (desc->N > 0 && (!Qx || !Kx || !V || !g || !beta || !out)) return GMA_ERR_INVALID_ARG;
+    const void *const ptrs[] = {Qx, Kx, V, g, beta, lengths, slots, state, out, workspace};
+    if (!all_aligned(ptrs)) return GMA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kHeaderBytes) return GMA_ERR_WORKSPACE;
+    if (desc->N == 0) return GMA_OK;
+    const DeltaProblem p = problem(desc, Qx, Kx, V, g, beta, lengths, workspace);
+    DeltaRec r{};
+    r.state_in = r.state_out = state;
+    r.slots = slots;
+    r.n_states = n_states;
+    r.out = out;
+    return launched(delta_rec_forward(p, r, static_cast<cudaStream_t>(stream)));
+}
+
+gma_status gma_delta_backward_workspace_size(const gma_delta_desc *desc, size_t *bytes) {
+    const gma_status st = validate(desc);
+    if (st != GMA_OK) return st;
+    if (!bytes) return GMA_ERR_INVALID_ARG;
+    *bytes = backward_layout(desc).total;
+    return GMA_OK;
+}
+
+gma_status gma_delta_backward(const gma_delta_desc *desc, const void *Qx, const void *Kx, const void *V, const void *g,
+                              const void *beta, const int *lengths, const float *state_in, const void *dO,
+                              const float *dstate_out, void *dQx, void *dKx, void *dV, void *dg, void *dbeta,
+                              float *dstate_in, void *workspace, size_t workspace_bytes, void *stream) {
+    const gma_status st = validate(desc);
+    if (st != GMA_OK) return st;
+    if (desc->N > 0 && (!Qx || !Kx || !V || !g || !beta || !dO || !dQx || !dKx || !dV || !dg || !dbeta))
+        return GMA_ERR_INVALID_ARG;
+    const void *const ptrs[] = {Qx, Kx, V, g, beta, lengths, state_in, dO, dstate_out, dQx, dKx, dV, dg, dbeta,
+                                dstate_in, workspace};
+    if (!all_aligned(ptrs)) return GMA_ERR_INVALID_ARG;
+    const BwdLayout2 L = backward_layout(desc);
+    if (!workspace || workspace_bytes < L.total) return GMA_ERR_WORKSPACE;
+    if (desc->N == 0 && (!dstate_in || dstate_in == dstate_out)) return GMA_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    auto at = [&](size_t o) { return reinterpret_cast<float *>(ws + o); };
+    DeltaProblem p = problem(desc, Qx, Kx, V, g, beta, lengths, workspace);
+
+    cudaError_t e;
+    if (desc->N > 0) {
+        // the states before each chunk and w of each row; its O goes where dV will be written
+        DeltaRec f{};
+        f.state_in = state_in;
+        f.out = dV;
+        f.rows_out = at(L.w);
+        f.ckpt = at(L.s0);
+        if ((e = delta_rec_forward(p, f, s)) != cudaSuccess) return launched(e);
+    }
+    DeltaProblem pb = p;
+    pb.V = dO;
+    DeltaRec r{};
+    r.state_in = dstate_out;
+    r.state_out = dstate_in;
+    r.out = dV;
+    r.rows_out = at(L.du);
+    r.ckpt = at(L.ds);
+    if ((e = delta_rec_backward(pb, r, s)) != cudaSuccess) return launched(e);
+    if (desc->N == 0) return GMA_OK;
+    const bool shared = desc->H != desc->Hk;
+    const DeltaGrads ga{dO, at(L.w), at(L.du), at(L.s0), at(L.ds), shared ? at(L.dq) : nullptr,
+                        shared ? at(L.dk) : nullptr, dQx, dKx, dg, dbeta};
+    if ((e = delta_rec_grads(p, ga, s)) != cudaSuccess) return launched(e);
+    if (shared) e = delta_sum_heads(p, at(L.dq), at(L.dk), dQx, dKx, s);
+    return launched(e);
+}
+
+static gma_status state_check(const gma_state_desc *d, const float *state, const int *src, const int *dst,
+                              const signed char *codes, const float *scales, void *ws, size_t wsb) {
+    if (!d || d->n < 0 || d->rows <= 0 || d->cols <= 0 || d->n_states <= 0 || d->n_cache <= 0) return GMA_ERR_INVALID_ARG;
+    if (!state || !codes || !scales) return GMA_ERR_INVALID_ARG;
+    // without indices entry i is at i
+    const bool store_like = src == nullptr || dst == nullptr;
+    if (store_like && d->n > (d->n_states < d->n_cache ? d->n_states : d->n_cache)) return GMA_ERR_INVALID_ARG;
+    const void *const ptrs[] = {state, src, dst, codes, scales, ws};
+    if (!all_aligned(ptrs)) return GMA_ERR_INVALID_ARG;
+    if ((long long)d->rows * d->cols > INT_MAX || d->n > 65535) return GMA_ERR_UNSUPPORTED;
+    if (!ws || wsb < kHeaderBytes) return GMA_ERR_WORKSPACE;
+    return GMA_OK;
+}
+
+static StateCopy state_problem(const gma_state_desc *d, const int *src, const int *dst, void *ws) {
+    return StateCopy{d->n, d->n_states, d->n_cache, d->rows, d->cols, src, dst, static_cast<unsigned *>(ws)};
+}
+
+gma_status gma_state_store(const gma_state_desc *desc, const float *state, const int *src, const int *dst,
+                           signed char *codes, float *scales, void *workspace, size_t workspace_bytes, void *stream) {
+    const gma_status st = state_check(desc, state, src, dst, codes, scales, workspace, workspace_bytes);
+    if (st != GMA_OK || desc->n == 0) return st;
+    return launched(state_store(state_problem(desc, src, dst, workspace), state, codes, scales,
+                                static_cast<cudaStream_t>(stream)));
+}
+
+gma_status gma_state_load(const gma_state_desc *desc, const signed char *codes, const float *scales, const int *src,
+                          const int *dst, float *state, void *workspace, size_t workspace_bytes, void *stream) {
+    const gma_status st = state_check(desc, state, src, dst, codes, scales, workspace, workspace_bytes);
+    if (st != GMA_OK || desc->n == 0) return st;
+    return launched(state_load(state_problem(desc, src, dst, workspace), codes, scales, state,
+                               static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

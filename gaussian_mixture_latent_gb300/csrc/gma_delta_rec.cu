@@ -1,0 +1,547 @@
+// The gated delta rule row by row, in fp32 on the CUDA cores: any d, dv <= 256, any length, both directions.
+//
+// Forward, per head, with the state S [d, dv] and decay a_t = e^{g_t}:
+//   w_t = v_t - a_t S^T k_t,  u_t = beta_t w_t,  S <- a_t S + k_t u_t^T,
+//   o_t = scale S_new^T q_t = scale (a_t S_old^T q_t + (q_t . k_t) u_t)
+// so both products of a row are against the old state and share one reduction.
+//
+// Backward, rows in reverse, with R = dL/dS after the row:
+//   du_t = R^T k_t + scale (q_t . k_t) dO_t   (R before dO_t's own term is added)
+//   x_t  = beta_t du_t = dV_t,   R <- a_t (R + scale q_t dO_t^T - k_t x_t^T).
+//
+// One CTA of 256 threads holds a [d, VW] slice of the state in registers: a thread has four neighbouring columns of
+// R rows, a warp reads whole row pieces of VW floats, and a row's column sums go over the 8 warps through shared
+// memory (one barrier a row, two buffers).  With one row (decoding) the time is the state's read and write; a long
+// sequence is bound by the latency of the chain (reduce, barrier, update) of each row.
+#include <cstdint>
+
+#include "gma_delta.h"
+
+namespace gma {
+namespace {
+
+constexpr int kThreads = 256, kWarps = 8, kTok = 8;      // kTok: rows staged at a time, one q.k dot to a warp
+
+struct RecArgs {
+    DeltaProblem p;
+    DeltaRec r;
+    int slices, tok;
+};
+
+template <typename In, int VW, int R, bool BWD>
+__global__ void __launch_bounds__(kThreads) delta_rec_kernel(const RecArgs a) {
+    constexpr int kLanes = VW / 4, kRowsWarp = 32 / kLanes;   // lanes of one row piece; row pieces of a warp
+    extern __shared__ __align__(16) float sm[];
+    const DeltaProblem &p = a.p;
+    const int d = p.d, dv = p.dv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int d4 = (d + 3) & ~3;
+    const int pitch = 2 * d4 + VW;
+    float *tok = sm;                                     // [a.tok][q | k | v]
+    float *part = tok + a.tok * pitch;                   // [2][2][kWarps][VW]
+    __shared__ float s_a[kTok], s_beta[kTok], s_qk[kTok];
+    const int slice = blockIdx.x % a.slices;
+    const int bh = blockIdx.x / a.slices, b = bh / p.H, h = bh % p.H;
+    const int hk = h / (p.H / p.Hk);
+    const int c0 = slice * VW + (lane % kLanes) * 4, rsub = lane / kLanes;
+    const int len = delta_len(p.lengths, b, p.N);
+
+    int slot = b;
+    bool mine = true;
+    if (a.r.slots) {
+        // a negative slot marks a batch entry that is not there; a slot outside the pool, or one that an earlier
+        // entry already has, is an error: either way the entry touches no state
+        slot = a.r.slots[b];
+        bool twice = false;
+        for (int j = tid; j < b; j += kThreads) twice |= a.r.slots[j] == slot;
+        twice = __syncthreads_or(twice);
+        const bool bad = slot >= a.r.n_states || (slot >= 0 && twice);
+        if (bad && tid == 0) atomicOr(p.status, (unsigned)kDevErrBounds);
+        mine = slot >= 0 && !bad;
+    }
+    const size_t head_rows = (size_t)bh * p.N;
+    const size_t key_rows = ((size_t)b * p.Hk + hk) * p.N;
+    In *out = static_cast<In *>(a.r.out);
+    const int live = mine ? len : 0;
+    // rows that do not exist are written as zeros
+    for (size_t i = tid; i < (size_t)(p.N - live) * VW; i += kThreads) {
+        const int c = slice * VW + (int)(i % VW);
+        if (c < dv) delta_out(out, (head_rows + live + i / VW) * dv + c, 0.f);
+    }
+    if (!mine) return;
+
+    float S[R][4];
+    const bool vec = (dv & 3) == 0;
+    const size_t sbase = ((size_t)slot * p.H + h) * d * dv;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int r = (i * kWarps + warp) * kRowsWarp + rsub;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[i][j] = 0.f;
+        if (a.r.state_in && r < d) {
+            const float *src = a.r.state_in + sbase + (size_t)r * dv + c0;
+            if (vec) {
+                if (c0 < dv) *reinterpret_cast<float4 *>(S[i]) = *reinterpret_cast<const float4 *>(src);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c0 + j < dv) S[i][j] = src[j];
+            }
+        }
+    }
+    auto write_state = [&](float *dst) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = (i * kWarps + warp) * kRowsWarp + rsub;
+            if (r >= d) continue;
+            float *to = dst + (size_t)r * dv + c0;
+            if (vec) {
+                if (c0 < dv) *reinterpret_cast<float4 *>(to) = *reinterpret_cast<float4 *>(S[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c0 + j < dv) to[j] = S[i][j];
+            }
+        }
+    };
+    const int nchunk = (p.N + kRecChunk - 1) / kRecChunk;
+    float *ckpt = a.r.ckpt ? a.r.ckpt + (size_t)bh * nchunk * d * dv : nullptr;
+
+    const In *Q = static_cast<const In *>(p.Qx), *K = static_cast<const In *>(p.Kx), *V = static_cast<const In *>(p.V);
+    for (int done = 0; done < len; done += a.tok) {
+        const int nt = min(a.tok, len - done);
+        __syncthreads();                                 // the last block's rows have been read
+        for (int i = tid; i < nt * pitch; i += kThreads) {
+            const int t = i / pitch, e = i % pitch;
+            const int row = BWD ? len - 1 - done - t : done + t;
+            float x = 0.f;
+            if (e < 2 * d4) {
+                const int c = e < d4 ? e : e - d4;
+                if (c < d) x = delta_in(e < d4 ? Q : K, (key_rows + row) * d + c);
+            } else {
+                const int c = slice * VW + e - 2 * d4;
+                if (c < dv) x = delta_in(V, (head_rows + row) * dv + c);
+            }
+            tok[i] = x;
+        }
+        if (tid < nt) {
+            const int row = BWD ? len - 1 - done - tid : done + tid;
+            s_a[tid] = expf(delta_gate(p.g, head_rows + row, p.gate_bf16));
+            s_beta[tid] = delta_gate(p.beta, head_rows + row, p.gate_bf16);
+        }
+        __syncthreads();
+        if (warp < nt) {
+            const float *q = tok + warp * pitch, *k = q + d4;
+            float x = 0.f;
+            for (int i = lane; i < d; i += 32) x = fmaf(q[i], k[i], x);
+            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+            if (lane == 0) s_qk[warp] = x;
+        }
+        for (int t = 0; t < nt; ++t) {
+            const int row = BWD ? len - 1 - done - t : done + t;
+            if (ckpt) {
+                if (!BWD && row % kRecChunk == 0) write_state(ckpt + (size_t)(row / kRecChunk) * d * dv);
+                if (BWD && (row % kRecChunk == kRecChunk - 1 || row == len - 1))
+                    write_state(ckpt + (size_t)(row / kRecChunk) * d * dv);
+            }
+            const float *q = tok + t * pitch, *k = q + d4;
+            float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int r = (i * kWarps + warp) * kRowsWarp + rsub;
+                const float kr = r < d ? k[r] : 0.f, qr = !BWD && r < d ? q[r] : 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    pk[j] = fmaf(kr, S[i][j], pk[j]);
+                    if (!BWD) pq[j] = fmaf(qr, S[i][j], pq[j]);
+                }
+            }
+#pragma unroll
+            for (int o = 16; o >= kLanes; o >>= 1)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    pk[j] += __shfl_xor_sync(~0u, pk[j], o);
+                    if (!BWD) pq[j] += __shfl_xor_sync(~0u, pq[j], o);
+                }
+            float *pb = part + (t & 1) * 2 * kWarps * VW;
+            const int cl = (lane % kLanes) * 4;
+            if (rsub == 0) {
+                *reinterpret_cast<float4 *>(pb + warp * VW + cl) = make_float4(pk[0], pk[1], pk[2], pk[3]);
+                if (!BWD)
+                    *reinterpret_cast<float4 *>(pb + (kWarps + warp) * VW + cl) = make_float4(pq[0], pq[1], pq[2], pq[3]);
+            }
+            __syncthreads();
+            float ks[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 x = *reinterpret_cast<const float4 *>(pb + w * VW + cl);
+                ks[0] += x.x; ks[1] += x.y; ks[2] += x.z; ks[3] += x.w;
+            }
+            const float dec = s_a[t], beta = s_beta[t], qk = s_qk[t];
+            const float4 v4 = *reinterpret_cast<const float4 *>(tok + t * pitch + 2 * d4 + cl);
+            const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+            float y[4], u[4];                            // forward: w, u; backward: du, x
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[j] = BWD ? fmaf(p.scale * qk, v[j], ks[j]) : fmaf(-dec, ks[j], v[j]);
+                u[j] = beta * y[j];
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int r = (i * kWarps + warp) * kRowsWarp + rsub;
+                const float kr = r < d ? k[r] : 0.f;
+                if (BWD) {
+                    const float qr = r < d ? p.scale * q[r] : 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[i][j] = dec * fmaf(-kr, u[j], fmaf(qr, v[j], S[i][j]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[i][j] = fmaf(kr, u[j], dec * S[i][j]);
+                }
+            }
+            if (warp == t && rsub == 0) {                // one warp a row writes the results (kTok <= kWarps)
+                float o[4];
+                if (BWD) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[j] = u[j];
+                } else {
+                    float qs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float4 x = *reinterpret_cast<const float4 *>(pb + (kWarps + w) * VW + cl);
+                        qs[0] += x.x; qs[1] += x.y; qs[2] += x.z; qs[3] += x.w;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[j] = p.scale * fmaf(dec, qs[j], qk * u[j]);
+                }
+                const size_t at = (head_rows + row) * dv + c0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c0 + j < dv) {
+                        delta_out(out, at + j, o[j]);
+                        if (a.r.rows_out) a.r.rows_out[at + j] = y[j];
+                    }
+            }
+        }
+    }
+    if (a.r.state_out) write_state(a.r.state_out + sbase);
+}
+
+template <typename In, int VW, int R, bool BWD>
+cudaError_t launch_rec(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
+    RecArgs a{p, r, (p.dv + VW - 1) / VW, p.N < kTok ? p.N : kTok};
+    const int d4 = (p.d + 3) & ~3;
+    const size_t smem = sizeof(float) * ((size_t)a.tok * (2 * d4 + VW) + 4 * kWarps * VW);
+    delta_rec_kernel<In, VW, R, BWD><<<(unsigned)((size_t)p.B * p.H * a.slices), kThreads, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+// The slice width: for one or a few rows the state's traffic is everything, so a CTA takes whole rows (up to 128
+// columns).  For longer sequences the chain of each row is: narrow slices (32 columns) give four times the CTAs and a
+// quarter of the state to each.
+template <typename In, bool BWD>
+cudaError_t rec_dispatch(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
+    if (p.N > kTok) {
+        if (p.d <= 64) return launch_rec<In, 32, 2, BWD>(p, r, s);
+        if (p.d <= 128) return launch_rec<In, 32, 4, BWD>(p, r, s);
+        return launch_rec<In, 32, 8, BWD>(p, r, s);
+    }
+    if (p.dv <= 64 || p.d > 128) {
+        if (p.d <= 64) return launch_rec<In, 64, 4, BWD>(p, r, s);
+        if (p.d <= 128) return launch_rec<In, 64, 8, BWD>(p, r, s);
+        return launch_rec<In, 64, 16, BWD>(p, r, s);
+    }
+    if (p.d <= 64) return launch_rec<In, 128, 8, BWD>(p, r, s);
+    return launch_rec<In, 128, 16, BWD>(p, r, s);
+}
+
+// ----------------------------------------------------------------------------------------------------------------
+// Gradients of Qx, Kx, g, beta from the states before and the state gradients after each chunk of 32 rows.  With
+// G the running sum of g in the chunk, D_ij = e^{G_i - G_j}, S0 the state before, R the gradient after the chunk,
+// u = beta w, x = beta du:
+//   dq_i = scale (e^{G_i} S0 dO_i + sum_{j<=i} D_ij (dO_i.u_j) k_j)
+//   dk_i = -(e^{G_i} S0 x_i + sum_{j<i} D_ij (x_i.u_j) k_j)
+//          + sum_{l>=i} scale D_li (dO_l.u_i) q_l - sum_{l>i} D_li (x_l.u_i) k_l + e^{G_C - G_i} R u_i
+//   dbeta_i = du_i . w_i
+//   dg_t = sum_{i>=t>j} M_ij + sum_{i>=t} e^{G_i} (scale q_i.S0 dO_i - k_i.S0 x_i) + sum_{j<t} e^{G_C-G_j} k_j.R u_j
+//          + e^{G_C} <S0, R>,   M_ij = D_ij (scale (dO_i.u_j)(q_i.k_j) - (x_i.u_j)(k_i.k_j))
+// The first sum is taken as running sums of (row sums - column sums) of M over the rows i, j; pairs with both rows
+// on one side of t then cancel as the same numbers in fp32.
+constexpr int kGThreads = 256;
+constexpr int C = kRecChunk;
+
+__host__ __device__ inline int grad_pitch(int n) {       // floats; an odd number of float4s keeps rows on other banks
+    const int q = (n + 3) / 4;
+    return 4 * (q | 1);
+}
+
+struct GradArgs {
+    DeltaProblem p;
+    DeltaGrads a;
+};
+
+__device__ __forceinline__ float dot4(const float *x, const float *y, int n4) {
+    float s = 0.f;
+    for (int i = 0; i < n4; ++i) {
+        const float4 a = reinterpret_cast<const float4 *>(x)[i], b = reinterpret_cast<const float4 *>(y)[i];
+        s = fmaf(a.x, b.x, s); s = fmaf(a.y, b.y, s); s = fmaf(a.z, b.z, s); s = fmaf(a.w, b.w, s);
+    }
+    return s;
+}
+
+template <typename In>
+__global__ void __launch_bounds__(kGThreads) delta_rec_grads_kernel(const GradArgs ga) {
+    extern __shared__ __align__(16) float sm[];
+    const DeltaProblem &p = ga.p;
+    const DeltaGrads &A = ga.a;
+    const int d = p.d, dv = p.dv, pd = grad_pitch(d), pv = grad_pitch(dv), tid = threadIdx.x;
+    const int d4 = (d + 3) / 4, v4 = (dv + 3) / 4;
+    float *q = sm, *k = q + C * pd, *dO = k + C * pd, *u = dO + C * pv, *x = u + C * pv;
+    float *E1 = x + C * pv, *E2 = E1 + C * (C + 1), *red = E2 + C * (C + 1);   // red: [8 warps][C][2]
+    __shared__ float hi[C], lo[C], beta[C], e0[C], f1[C], rowM[C], colM[C], dbeta[C], inner[8];
+    __shared__ double gsum[C];
+    const int nchunk = (p.N + C - 1) / C;
+    const int c = blockIdx.x % nchunk, bh = blockIdx.x / nchunk, b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
+    const int len = delta_len(p.lengths, b, p.N), row0 = c * C;
+    const int n = min(max(len - row0, 0), C), all = min(C, p.N - row0);
+    const size_t head_rows = (size_t)bh * p.N + row0, key_rows = ((size_t)b * p.Hk + hk) * p.N + row0;
+
+    for (int i = tid; i < C * pd; i += kGThreads) {
+        const int t = i / pd, e = i % pd;
+        const bool ok = t < n && e < d;
+        q[i] = ok ? delta_in(static_cast<const In *>(p.Qx), (key_rows + t) * d + e) : 0.f;
+        k[i] = ok ? delta_in(static_cast<const In *>(p.Kx), (key_rows + t) * d + e) : 0.f;
+    }
+    if (tid < C) {
+        double g = tid < n ? (double)delta_floor(delta_gate(p.g, head_rows + tid, p.gate_bf16)) * 1.4426950408889634 : 0.0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(~0u, g, o);
+            if (tid >= o) g += y;
+        }
+        gsum[tid] = g;
+        hi[tid] = (float)g;
+        lo[tid] = (float)(g - (double)hi[tid]);
+        beta[tid] = tid < n ? delta_gate(p.beta, head_rows + tid, p.gate_bf16) : 0.f;
+        e0[tid] = exp2f((float)g);
+        f1[tid] = exp2f((float)(__shfl_sync(~0u, g, 31) - g));
+    }
+    __syncthreads();
+    for (int i = tid; i < C * pv; i += kGThreads) {
+        const int t = i / pv, e = i % pv;
+        const bool ok = t < n && e < dv;
+        const size_t at = (head_rows + t) * dv + e;
+        dO[i] = ok ? delta_in(static_cast<const In *>(A.dO), at) : 0.f;
+        u[i] = ok ? A.w[at] : 0.f;                       // w and du first: dbeta is their product
+        x[i] = ok ? A.du[at] : 0.f;
+    }
+    __syncthreads();
+    for (int t = tid / 32; t < C; t += kGThreads / 32) {
+        float s = 0.f;
+        for (int e = tid % 32; e < dv; e += 32) s = fmaf(u[t * pv + e], x[t * pv + e], s);
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+        if (tid % 32 == 0) dbeta[t] = s;
+    }
+    __syncthreads();
+    for (int i = tid; i < C * pv; i += kGThreads) {
+        const float be = beta[i / pv];
+        u[i] *= be;
+        x[i] *= be;
+    }
+    __syncthreads();
+    // E1 = scale D o (dO U^T), E2 = D o (X U^T) strictly below the diagonal, and M's row and column sums
+    float m[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = tid / 8, j = tid % 8 + 8 * e;
+        float a1 = 0.f, a2 = 0.f;
+        m[e] = 0.f;
+        if (j <= i) {
+            const float D = exp2f((hi[i] - hi[j]) + (lo[i] - lo[j]));
+            a1 = p.scale * D * dot4(dO + i * pv, u + j * pv, v4);
+            m[e] = a1 * dot4(q + i * pd, k + j * pd, d4);
+            if (j < i) {
+                a2 = D * dot4(x + i * pv, u + j * pv, v4);
+                m[e] -= a2 * dot4(k + i * pd, k + j * pd, d4);
+            }
+        }
+        E1[i * (C + 1) + j] = a1;
+        E2[i * (C + 1) + j] = a2;
+    }
+    float *M = red;                                      // [C][C + 1], before `red` is used
+#pragma unroll
+    for (int e = 0; e < 4; ++e) M[(tid / 8) * (C + 1) + tid % 8 + 8 * e] = m[e];
+    __syncthreads();
+    if (tid < C) {
+        float s = 0.f;
+        for (int j = 0; j < C; ++j) s += M[tid * (C + 1) + j];
+        rowM[tid] = s;
+    } else if (tid < 2 * C) {
+        float s = 0.f;
+        for (int i = 0; i < C; ++i) s += M[i * (C + 1) + tid - C];
+        colM[tid - C] = s;
+    }
+    __syncthreads();
+    const float *S0 = A.s0 + ((size_t)bh * nchunk + c) * d * dv, *R = A.ds + ((size_t)bh * nchunk + c) * d * dv;
+    const int half = tid / 128, i0 = half * 16, warp = tid / 32, lane = tid % 32;
+    float acc_row[16], acc_key[16], in = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc_row[i] = acc_key[i] = 0.f;
+    In *dQ = static_cast<In *>(A.dQ), *dK = static_cast<In *>(A.dK);
+    if (n > 0)
+        for (int r = tid % 128; r < d; r += 128) {
+            float a1[16], a2[16], a3[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) a1[i] = a2[i] = a3[i] = 0.f;
+            for (int e = 0; e < dv; e += 4) {
+                float s0[4], ds[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s0[j] = e + j < dv ? S0[(size_t)r * dv + e + j] : 0.f;
+                    ds[j] = e + j < dv ? R[(size_t)r * dv + e + j] : 0.f;
+                    if (half == 0) in = fmaf(s0[j], ds[j], in);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 o = *reinterpret_cast<const float4 *>(dO + (i0 + i) * pv + e);
+                    const float4 y = *reinterpret_cast<const float4 *>(x + (i0 + i) * pv + e);
+                    const float4 z = *reinterpret_cast<const float4 *>(u + (i0 + i) * pv + e);
+                    a1[i] = fmaf(s0[0], o.x, fmaf(s0[1], o.y, fmaf(s0[2], o.z, fmaf(s0[3], o.w, a1[i]))));
+                    a2[i] = fmaf(s0[0], y.x, fmaf(s0[1], y.y, fmaf(s0[2], y.z, fmaf(s0[3], y.w, a2[i]))));
+                    a3[i] = fmaf(ds[0], z.x, fmaf(ds[1], z.y, fmaf(ds[2], z.z, fmaf(ds[3], z.w, a3[i]))));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int t = i0 + i;
+                a1[i] *= p.scale * e0[t];
+                a2[i] *= e0[t];
+                a3[i] *= f1[t];
+                const float qr = q[t * pd + r], kr = k[t * pd + r];
+                acc_row[i] += qr * a1[i] - kr * a2[i];
+                acc_key[i] += kr * a3[i];
+                float dq = a1[i], dk = a3[i] - a2[i];
+                for (int j = 0; j <= t; ++j) {
+                    const float kj = k[j * pd + r];
+                    dq = fmaf(E1[t * (C + 1) + j], kj, dq);
+                    dk = fmaf(-E2[t * (C + 1) + j], kj, dk);
+                }
+                for (int l = t; l < C; ++l) {
+                    dk = fmaf(E1[l * (C + 1) + t], q[l * pd + r], dk);
+                    dk = fmaf(-E2[l * (C + 1) + t], k[l * pd + r], dk);
+                }
+                if (t < all) {
+                    const size_t at = (head_rows + t) * d + r;
+                    if (A.dq_heads) {
+                        A.dq_heads[at] = dq;
+                        A.dk_heads[at] = dk;
+                    } else {
+                        delta_out(dQ, at, t < n ? dq : 0.f);
+                        delta_out(dK, at, t < n ? dk : 0.f);
+                    }
+                }
+            }
+        }
+    else
+        for (int i = tid; i < all * d; i += kGThreads) {
+            if (A.dq_heads) A.dq_heads[head_rows * d + i] = A.dk_heads[head_rows * d + i] = 0.f;
+            else {
+                delta_out(dQ, head_rows * d + i, 0.f);
+                delta_out(dK, head_rows * d + i, 0.f);
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        for (int o = 16; o; o >>= 1) {
+            acc_row[i] += __shfl_xor_sync(~0u, acc_row[i], o);
+            acc_key[i] += __shfl_xor_sync(~0u, acc_key[i], o);
+        }
+    for (int o = 16; o; o >>= 1) in += __shfl_xor_sync(~0u, in, o);
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            red[(warp * 16 + i) * 2] = acc_row[i];
+            red[(warp * 16 + i) * 2 + 1] = acc_key[i];
+        }
+        inner[warp] = in;
+    }
+    __syncthreads();
+    if (tid < C) {
+        // running sums over the rows in fp64: 32 values, and the sums before and after t may cancel
+        const int w0 = (tid / 16) * 4, i = tid % 16;
+        double ar = (double)rowM[tid] - (double)colM[tid], ak = 0.0, tot = 0.0;
+        for (int w = 0; w < 4; ++w) {
+            ar += red[((w0 + w) * 16 + i) * 2];
+            ak += red[((w0 + w) * 16 + i) * 2 + 1];
+            tot += inner[w];
+        }
+        double after = ar, before = ak;
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_down_sync(~0u, after, o), z = __shfl_up_sync(~0u, before, o);
+            if (tid + o < 32) after += y;
+            if (tid >= o) before += z;
+        }
+        // the last row of the chunk decides whether <S0, R> is reached at all
+        const float eC = exp2f((float)__shfl_sync(~0u, gsum[tid], 31));
+        const double dg = after + (before - ak) + (n > 0 ? (double)eC * tot : 0.0);
+        if (tid < all) {
+            // dg_t = e^{g_t} <dL/d(e^{g_t} S), S>: exactly 0 where the decay forgets everything, not the rounding of
+            // the two sums
+            const bool lives = tid < n && expf(delta_gate(p.g, head_rows + tid, p.gate_bf16)) != 0.f;
+            delta_gate_out(A.dg, head_rows + tid, lives ? (float)dg : 0.f, p.gate_bf16);
+            delta_gate_out(A.dbeta, head_rows + tid, tid < n ? dbeta[tid] : 0.f, p.gate_bf16);
+        }
+    }
+}
+
+template <typename In>
+__global__ void __launch_bounds__(256) delta_sum_heads_kernel(const float *dq, const float *dk, In *dQ, In *dK, int Hk,
+                                                              int r, size_t head, size_t total) {
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
+        const size_t bk = i / head, e = i % head;        // [B * Hk] key heads of `head` = N * d elements
+        const size_t first = bk * r * head + e;
+        float a = 0.f, b = 0.f;
+        for (int j = 0; j < r; ++j) {
+            a += dq[first + j * head];
+            b += dk[first + j * head];
+        }
+        delta_out(dQ, i, a);
+        delta_out(dK, i, b);
+    }
+}
+
+template <typename In>
+cudaError_t grads_launch(const DeltaProblem &p, const DeltaGrads &a, cudaStream_t s) {
+    const int nchunk = (p.N + C - 1) / C;
+    const int smem = (int)sizeof(float) * (C * (2 * grad_pitch(p.d) + 3 * grad_pitch(p.dv)) + 3 * C * (C + 1));
+    const cudaError_t e = set_dyn_smem((const void *)delta_rec_grads_kernel<In>, smem);
+    if (e != cudaSuccess) return e;
+    delta_rec_grads_kernel<In><<<(unsigned)((size_t)p.B * p.H * nchunk), kGThreads, smem, s>>>(GradArgs{p, a});
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t delta_rec_forward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
+    return p.bf16 ? rec_dispatch<__nv_bfloat16, false>(p, r, s) : rec_dispatch<float, false>(p, r, s);
+}
+
+cudaError_t delta_rec_backward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
+    return p.bf16 ? rec_dispatch<__nv_bfloat16, true>(p, r, s) : rec_dispatch<float, true>(p, r, s);
+}
+
+cudaError_t delta_rec_grads(const DeltaProblem &p, const DeltaGrads &a, cudaStream_t s) {
+    return p.bf16 ? grads_launch<__nv_bfloat16>(p, a, s) : grads_launch<float>(p, a, s);
+}
+
+cudaError_t delta_sum_heads(const DeltaProblem &p, const float *dq, const float *dk, void *dQ, void *dK,
+                            cudaStream_t s) {
+    const size_t head = (size_t)p.N * p.d, total = head * p.B * p.Hk;
+    const unsigned grid = (unsigned)(total / 256 + 1 < 152 * 16 ? total / 256 + 1 : 152 * 16);
+    if (p.bf16)
+        delta_sum_heads_kernel<<<grid, 256, 0, s>>>(dq, dk, (__nv_bfloat16 *)dQ, (__nv_bfloat16 *)dK, p.Hk, p.H / p.Hk,
+                                                    head, total);
+    else
+        delta_sum_heads_kernel<<<grid, 256, 0, s>>>(dq, dk, (float *)dQ, (float *)dK, p.Hk, p.H / p.Hk, head, total);
+    return cudaGetLastError();
+}
+
+}  // namespace gma

@@ -1,0 +1,198 @@
+// Carried states kept in 8 bits: quantised as they are written to a cache, and read back.
+//
+// A state is a matrix of `rows` rows (all heads) of `cols` fp32 values.  Each row is cut into groups of 32 from its
+// start (the last may be shorter), and a group keeps one fp32 scale:
+//   scale = max |x| / 127,   code = rint(x / scale) in [-127, 127],   read back as code * scale.
+// Both divisions are IEEE fp32 divisions: the format says which code a value on a border gets.  The error of a value
+// is at most half a step, max |x| / 254.  Rounding to 8 bits is the purpose of the cache; the recurrences themselves
+// keep their states in fp32.  In a [K, dv + 1] mixture memory whose dv is a multiple of 32 the normaliser column is a
+// group of its own and comes back to within one rounding.
+//
+// Bound by memory: 5.125 bytes an element (at cols a multiple of 32).  A thread takes four neighbouring elements (one
+// float4, one char4), eight threads a group, and kUnroll such pieces at a time so that enough loads are in flight.
+#include <cstdint>
+
+#include "gma_delta.h"
+
+namespace gma {
+namespace {
+
+constexpr int kThreads = 256, kGroup = 32, kSub = kGroup / 4, kUnroll = 4;
+
+struct CopyArgs {
+    StateCopy p;
+    float *state;
+    signed char *codes;
+    float *scales;
+    int groups;                       // groups of a row
+    long long pieces, per_cta;        // (row, group, sub) pieces of four elements: of a state, of one CTA
+    int ctas;                         // CTAs of one state
+};
+
+// The entry's source and destination, or false where there is nothing to copy: a negative index marks an absent entry, an index
+// outside its pool is an error, and of several entries with one destination the last one counts.
+__device__ bool copy_pair(const CopyArgs &a, int n_src, int n_dst, int i, int &src, int &dst) {
+    src = a.p.src ? a.p.src[i] : i;
+    dst = a.p.dst ? a.p.dst[i] : i;
+    bool later = false;
+    if (a.p.dst)
+        for (int j = i + 1 + threadIdx.x; j < a.p.n; j += kThreads)
+            later |= a.p.dst[j] == dst && (!a.p.src || (a.p.src[j] >= 0 && a.p.src[j] < n_src));
+    later = __syncthreads_or(later);
+    if (src >= n_src || dst >= n_dst) {
+        if (threadIdx.x == 0) atomicOr(a.p.status, (unsigned)kDevErrBounds);
+        return false;
+    }
+    return src >= 0 && dst >= 0 && !later;
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads) state_store_kernel(const CopyArgs a) {
+    int src, dst;
+    const int i = blockIdx.x / a.ctas;
+    if (!copy_pair(a, a.p.n_states, a.p.n_cache, i, src, dst)) return;
+    const float *from = a.state + (size_t)src * a.p.rows * a.p.cols;
+    signed char *codes = a.codes + (size_t)dst * a.p.rows * a.p.cols;
+    float *scales = a.scales + (size_t)dst * a.p.rows * a.groups;
+    const long long first = (long long)(blockIdx.x % a.ctas) * a.per_cta;
+    const long long last = min(first + a.per_cta, a.pieces);
+    // `first` and `last` are multiples of kSub: the eight threads of a group are there together
+    for (long long at = first + threadIdx.x; at - threadIdx.x < last; at += (long long)kThreads * kUnroll) {
+        float x[kUnroll][4];
+        long long off[kUnroll], grp[kUnroll];
+        int n[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const long long w = at + (long long)u * kThreads;
+            const bool in = w < last;
+            grp[u] = in ? w / kSub : 0;
+            const long long row = grp[u] / a.groups;
+            const int col = (int)(grp[u] % a.groups) * kGroup + (int)(w % kSub) * 4;
+            n[u] = in ? min(max(a.p.cols - col, 0), 4) : 0;
+            off[u] = row * a.p.cols + col;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[u][j] = 0.f;
+            if (VEC) {
+                if (n[u]) *reinterpret_cast<float4 *>(x[u]) = __ldcs(reinterpret_cast<const float4 *>(from + off[u]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < n[u]) x[u][j] = from[off[u] + j];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const bool in = at + (long long)u * kThreads < last;
+            float m = 0.f;
+            bool odd = false;                            // a NaN or an infinity in the group
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                m = fmaxf(m, fabsf(x[u][j]));
+                odd |= !(fabsf(x[u][j]) <= 3.402823466e38f);
+            }
+#pragma unroll
+            for (int o = 1; o < kSub; o <<= 1) {
+                m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+                odd |= __shfl_xor_sync(~0u, (int)odd, o) != 0;
+            }
+            const float scale = __fdiv_rn(m, 127.f);
+            signed char q[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // a scale that underflows to zero leaves zeros; one that was rounded down as a subnormal is why the
+                // quotient is held within 127
+                const float y = odd || scale == 0.f ? 0.f : rintf(__fdiv_rn(x[u][j], scale));
+                q[j] = (signed char)(int)fminf(fmaxf(y, -127.f), 127.f);
+            }
+            if (VEC) {
+                if (n[u]) *reinterpret_cast<char4 *>(codes + off[u]) = make_char4(q[0], q[1], q[2], q[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < n[u]) codes[off[u] + j] = q[j];
+            }
+            if (in && threadIdx.x % kSub == 0) scales[grp[u]] = odd ? __int_as_float(0x7fffffff) : scale;
+        }
+    }
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads) state_load_kernel(const CopyArgs a) {
+    int src, dst;
+    const int i = blockIdx.x / a.ctas;
+    if (!copy_pair(a, a.p.n_cache, a.p.n_states, i, src, dst)) return;
+    const signed char *codes = a.codes + (size_t)src * a.p.rows * a.p.cols;
+    const float *scales = a.scales + (size_t)src * a.p.rows * a.groups;
+    float *to = a.state + (size_t)dst * a.p.rows * a.p.cols;
+    const long long first = (long long)(blockIdx.x % a.ctas) * a.per_cta;
+    const long long last = min(first + a.per_cta, a.pieces);
+    for (long long at = first + threadIdx.x; at < last; at += (long long)kThreads * kUnroll) {
+        char4 q[kUnroll];
+        float scale[kUnroll];
+        long long off[kUnroll];
+        int n[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const long long w = at + (long long)u * kThreads;
+            const long long grp = w < last ? w / kSub : 0, row = grp / a.groups;
+            const int col = (int)(grp % a.groups) * kGroup + (int)(w % kSub) * 4;
+            n[u] = w < last ? min(max(a.p.cols - col, 0), 4) : 0;
+            off[u] = row * a.p.cols + col;
+            q[u] = make_char4(0, 0, 0, 0);
+            if (VEC) {
+                if (n[u]) q[u] = *reinterpret_cast<const char4 *>(codes + off[u]);
+            } else {
+                if (n[u] > 0) q[u].x = codes[off[u]];
+                if (n[u] > 1) q[u].y = codes[off[u] + 1];
+                if (n[u] > 2) q[u].z = codes[off[u] + 2];
+                if (n[u] > 3) q[u].w = codes[off[u] + 3];
+            }
+            scale[u] = n[u] ? scales[grp] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const float4 x = make_float4(q[u].x * scale[u], q[u].y * scale[u], q[u].z * scale[u], q[u].w * scale[u]);
+            if (VEC) {
+                if (n[u]) *reinterpret_cast<float4 *>(to + off[u]) = x;
+            } else {
+                if (n[u] > 0) to[off[u]] = x.x;
+                if (n[u] > 1) to[off[u] + 1] = x.y;
+                if (n[u] > 2) to[off[u] + 2] = x.z;
+                if (n[u] > 3) to[off[u] + 3] = x.w;
+            }
+        }
+    }
+}
+
+CopyArgs copy_args(const StateCopy &p, float *state, signed char *codes, float *scales) {
+    CopyArgs a{p, state, codes, scales, (p.cols + kGroup - 1) / kGroup, 0, 0, 0};
+    a.pieces = p.rows * a.groups * kSub;
+    // eight rounds of the unrolled loop to a CTA; fewer where that would leave most of the GPU idle
+    long long rounds = 8;
+    while (rounds > 1 && (long long)p.n * ((a.pieces + rounds * kThreads * kUnroll - 1) / (rounds * kThreads * kUnroll)) < 608)
+        rounds /= 2;
+    a.per_cta = rounds * kThreads * kUnroll;
+    a.ctas = (int)((a.pieces + a.per_cta - 1) / a.per_cta);
+    return a;
+}
+
+}  // namespace
+
+cudaError_t state_store(const StateCopy &p, const float *state, signed char *codes, float *scales, cudaStream_t s) {
+    const CopyArgs a = copy_args(p, const_cast<float *>(state), codes, scales);
+    const unsigned grid = (unsigned)((long long)a.ctas * p.n);
+    if (p.cols % 4 == 0) state_store_kernel<true><<<grid, kThreads, 0, s>>>(a);
+    else state_store_kernel<false><<<grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t state_load(const StateCopy &p, const signed char *codes, const float *scales, float *state,
+                       cudaStream_t s) {
+    const CopyArgs a = copy_args(p, state, const_cast<signed char *>(codes), const_cast<float *>(scales));
+    const unsigned grid = (unsigned)((long long)a.ctas * p.n);
+    if (p.cols % 4 == 0) state_load_kernel<true><<<grid, kThreads, 0, s>>>(a);
+    else state_load_kernel<false><<<grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace gma

@@ -1,0 +1,268 @@
+"""The gated delta rule and the 8-bit state cache: the binding of their part of ``include/gma.h``.
+
+Per batch entry and value head (key head h // (H // Hk)), with a float32 state S [d, dv]:
+    w_t = V_t - exp(g_t) S^T Kx_t,   S <- exp(g_t) S + Kx_t (beta_t w_t)^T,   out_t = scale S^T Qx_t.
+
+The functions check and marshal torch tensors; the computation is in the library's kernels.  Tensors are on
+one CUDA device, which is made current for the call; the call runs on `stream`, or on that device's current
+stream.  Scratch memory: `workspace` (uint8, of the size that the library asks for, its first 256 bytes zero),
+or a buffer kept per device and stream; while a CUDA graph is captured, a buffer of the graph's own.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+import gaussian_mixture_latent_gb300 as _gma
+
+
+class gma_delta_desc(ctypes.Structure):
+    """Mirror of ``gma_delta_desc`` in include/gma.h."""
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("N", ctypes.c_int),
+                ("d", ctypes.c_int), ("dv", ctypes.c_int), ("in_dtype", ctypes.c_int),
+                ("gate_dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class gma_state_desc(ctypes.Structure):
+    """Mirror of ``gma_state_desc`` in include/gma.h."""
+    _fields_ = [("n", ctypes.c_int), ("n_states", ctypes.c_int), ("n_cache", ctypes.c_int),
+                ("rows", ctypes.c_int), ("cols", ctypes.c_int)]
+
+
+_signed = False
+
+
+def _lib():
+    global _signed
+    lib = _gma._load()
+    if not _signed:
+        vp, sz, i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+        dp, sp, zp = ctypes.POINTER(gma_delta_desc), ctypes.POINTER(gma_state_desc), ctypes.POINTER(sz)
+        for name in ("gma_delta_workspace_size", "gma_delta_backward_workspace_size", "gma_delta_decode_workspace_size"):
+            getattr(lib, name).argtypes = [dp, zp]
+        lib.gma_delta_forward.argtypes = [dp] + [vp] * 9 + [vp, sz, vp]
+        lib.gma_delta_backward.argtypes = [dp] + [vp] * 15 + [vp, sz, vp]
+        lib.gma_delta_decode.argtypes = [dp] + [vp] * 7 + [i, vp, vp, vp, sz, vp]
+        lib.gma_state_store.argtypes = [sp] + [vp] * 5 + [vp, sz, vp]
+        lib.gma_state_load.argtypes = [sp] + [vp] * 5 + [vp, sz, vp]
+        _signed = True
+    return lib
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_scratch: dict = {}
+
+
+def _check(t, name, shape, dtypes, device):
+    _gma._check(t, name, shape, dtypes)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+class _Call:
+    """The device, stream and workspace of one call."""
+
+    def __init__(self, what, device, stream, workspace):
+        if not isinstance(device, torch.device) or device.type != "cuda":
+            raise ValueError(f"{what}: tensors must be CUDA tensors")
+        self.what, self.device, self.workspace = what, device, workspace
+        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
+        if self.stream.device != device:
+            raise ValueError(f"{what}: the stream is on {self.stream.device}, the tensors on {device}")
+
+    def run(self, fn, need, args, check_status):
+        with torch.cuda.device(self.device), torch.cuda.stream(self.stream):
+            ws = self._workspace(need)
+            rc = fn(*args, ws.data_ptr(), ws.numel(), self.stream.cuda_stream)
+            if rc:
+                raise _gma.GmaError(rc, self.what)
+            if check_status:
+                _gma._check_device_status(ws, self.stream, self.what)
+
+    def _workspace(self, need):
+        ws = self.workspace
+        if ws is not None:
+            if not ws.is_cuda or ws.device != self.device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+                raise ValueError(f"{self.what}: workspace must be a contiguous uint8 tensor on {self.device}")
+            if ws.numel() < need:
+                raise _gma.GmaError(3, self.what)
+            return ws
+        key = (self.device.index, self.stream.cuda_stream)
+        capturing = torch.cuda.is_current_stream_capturing()
+        ws = None if capturing else _scratch.get(key)
+        if ws is None or ws.numel() < need:
+            # allocated on the call's own stream, so that a buffer that is replaced is reused in its order
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+            _gma.gma_workspace_init(ws, self.stream)
+            if not capturing:
+                _scratch[key] = ws
+        return ws
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _sequence(what, Qx, Kx, V, g, beta, lengths, scale, stream, workspace):
+    """The checked description and call of one gated-delta-rule problem."""
+    for name, t, dims in (("Qx", Qx, 4), ("V", V, 4)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != dims:
+            raise ValueError(f"{name} has {t.dim()} dimensions, expected {dims}")
+    if not isinstance(g, torch.Tensor):
+        raise TypeError("g must be a torch.Tensor")
+    B, Hk, N, d = Qx.shape
+    H, dv = V.shape[1], V.shape[3]
+    dev = Qx.device
+    call = _Call(what, dev, stream, workspace)
+    _check(Qx, "Qx", (B, Hk, N, d), _FLOATS, dev)
+    _check(Kx, "Kx", (B, Hk, N, d), (Qx.dtype,), dev)
+    _check(V, "V", (B, H, N, dv), (Qx.dtype,), dev)
+    _check(g, "g", (B, H, N), _FLOATS, dev)
+    _check(beta, "beta", (B, H, N), (g.dtype,), dev)
+    if Hk == 0 or H % Hk:
+        raise ValueError(f"V has {H} heads, expected a multiple of Qx's {Hk}")
+    if lengths is not None:
+        _check(lengths, "lengths", (B,), (torch.int32,), dev)
+    scale = d ** -0.5 if scale is None else float(scale)
+    desc = gma_delta_desc(B, H, Hk, N, d, dv, _gma._DTYPES[Qx.dtype], _gma._DTYPES[g.dtype], scale)
+    return desc, call
+
+
+def _need(fn, desc, what):
+    n = ctypes.c_size_t(0)
+    rc = fn(ctypes.byref(desc), ctypes.byref(n))
+    if rc:
+        raise _gma.GmaError(rc, what)
+    return n.value
+
+
+def gma_delta_forward(Qx, Kx, V, g, beta, state=None, lengths=None, scale=None, return_state: bool = False, out=None,
+                      state_out=None, workspace=None, stream=None, check_status: bool = False):
+    """The gated delta rule over whole sequences.  Qx, Kx [B,Hk,N,d], V [B,H,N,dv] (float32 or
+    bfloat16; H a multiple of Hk), g (log decay) and beta [B,H,N] (float32 or bfloat16) ->
+    out [B,H,N,dv], or (out, state [B,H,d,dv] float32) with return_state or state_out.
+
+    `state` is the state before the first row (default zeros) and is not changed unless it is
+    also state_out.  Rows at and past lengths[b] (int32 [B]) do not exist: out is 0 there.
+    scale defaults to d ** -0.5."""
+    desc, call = _sequence("gma_delta_forward", Qx, Kx, V, g, beta, lengths, scale, stream, workspace)
+    lib = _lib()
+    need = _need(lib.gma_delta_workspace_size, desc, "gma_delta_forward")
+    shape = (desc.B, desc.H, desc.d, desc.dv)
+    with torch.cuda.device(call.device), torch.cuda.stream(call.stream):
+        if out is None:
+            out = torch.empty(V.shape, dtype=V.dtype, device=V.device)
+        if return_state and state_out is None:
+            state_out = torch.empty(shape, dtype=torch.float32, device=V.device)
+    _check(out, "out", tuple(V.shape), (V.dtype,), call.device)
+    for name, t in (("state", state), ("state_out", state_out)):
+        if t is not None:
+            _check(t, name, shape, (torch.float32,), call.device)
+    call.run(lib.gma_delta_forward, need,
+             (ctypes.byref(desc),) + tuple(_ptr(t) for t in (Qx, Kx, V, g, beta, lengths, state, out, state_out)),
+             check_status)
+    return out if state_out is None else (out, state_out)
+
+
+def gma_delta_backward(Qx, Kx, V, g, beta, dO, state=None, dstate=None, lengths=None, scale=None, grads=None,
+                       workspace=None, stream=None, check_status: bool = False):
+    """Gradient of gma_delta_forward(Qx, Kx, V, g, beta, state): given dO [B,H,N,dv] and, when the
+    returned state was used, dstate = dL/dstate [B,H,d,dv] float32, returns (dQx, dKx, dV, dg, dbeta,
+    dstate_in), each in its input's type; dstate_in (float32) is None when `state` is None.
+    `grads`, if given, is that tuple of preallocated outputs (overwritten)."""
+    desc, call = _sequence("gma_delta_backward", Qx, Kx, V, g, beta, lengths, scale, stream, workspace)
+    lib = _lib()
+    _check(dO, "dO", tuple(V.shape), (V.dtype,), call.device)
+    shape = (desc.B, desc.H, desc.d, desc.dv)
+    for name, t in (("state", state), ("dstate", dstate)):
+        if t is not None:
+            _check(t, name, shape, (torch.float32,), call.device)
+    need = _need(lib.gma_delta_backward_workspace_size, desc, "gma_delta_backward")
+    if grads is None:
+        with torch.cuda.device(call.device), torch.cuda.stream(call.stream):
+            grads = tuple(torch.empty_like(t) for t in (Qx, Kx, V, g, beta)) + (
+                None if state is None else torch.empty_like(state),)
+    for t, like, name in zip(grads, (Qx, Kx, V, g, beta, state), ("dQx", "dKx", "dV", "dg", "dbeta", "dstate_in")):
+        if like is not None:
+            _check(t, name, tuple(like.shape), (like.dtype,), call.device)
+    dstate_in = grads[5] if state is not None else None
+    call.run(lib.gma_delta_backward, need,
+             (ctypes.byref(desc),) + tuple(_ptr(t) for t in (Qx, Kx, V, g, beta, lengths, state, dO, dstate) +
+                                           tuple(grads[:5]) + (dstate_in,)), check_status)
+    return tuple(grads[:5]) + (dstate_in,)
+
+
+def gma_delta_decode(Qx, Kx, V, g, beta, state, slots=None, lengths=None, scale=None, out=None, workspace=None,
+                     stream=None, check_status: bool = False):
+    """The next N positions (one or a few) of sequences whose states lie in a pool: `state`
+    [S,H,d,dv] float32, updated in place; batch entry b uses state[slots[b]] (int32 [B]; default
+    state[b]).  A negative slot marks an absent entry: its out rows are 0.  A slot outside the
+    pool, or one that an earlier entry names, is treated so too and posts GMA_ERR_BOUNDS
+    (raised with check_status).  Returns out [B,H,N,dv]."""
+    desc, call = _sequence("gma_delta_decode", Qx, Kx, V, g, beta, lengths, scale, stream, workspace)
+    lib = _lib()
+    need = _need(lib.gma_delta_decode_workspace_size, desc, "gma_delta_decode")
+    if not isinstance(state, torch.Tensor):
+        raise TypeError("state must be a torch.Tensor")
+    if state.dim() != 4:
+        raise ValueError(f"state has {state.dim()} dimensions, expected 4")
+    _check(state, "state", (state.shape[0], desc.H, desc.d, desc.dv), (torch.float32,), call.device)
+    if slots is not None:
+        _check(slots, "slots", (desc.B,), (torch.int32,), call.device)
+    if out is None:
+        with torch.cuda.device(call.device), torch.cuda.stream(call.stream):
+            out = torch.empty(V.shape, dtype=V.dtype, device=V.device)
+    _check(out, "out", tuple(V.shape), (V.dtype,), call.device)
+    call.run(lib.gma_delta_decode, need,
+             (ctypes.byref(desc),) + tuple(_ptr(t) for t in (Qx, Kx, V, g, beta, lengths, slots)) +
+             (state.shape[0], _ptr(state), _ptr(out)), check_status)
+    return out
+
+
+def _cache(what, state, codes, scales, src, dst, stream, workspace):
+    for name, t in (("state", state), ("codes", codes)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != 4:
+            raise ValueError(f"{name} has {t.dim()} dimensions, expected 4")
+    dev = state.device
+    call = _Call(what, dev, stream, workspace)
+    S, H, R, cols = state.shape
+    P = codes.shape[0]
+    _check(state, "state", (S, H, R, cols), (torch.float32,), dev)
+    _check(codes, "codes", (P, H, R, cols), (torch.int8,), dev)
+    _check(scales, "scales", (P, H, R, (cols + 31) // 32), (torch.float32,), dev)
+    n = min(S, P)
+    for t in (src, dst):
+        if t is not None:
+            n = t.shape[0] if isinstance(t, torch.Tensor) and t.dim() == 1 else -1
+    for name, t in (("src", src), ("dst", dst)):
+        if t is not None:
+            _check(t, name, (n,), (torch.int32,), dev)
+    return gma_state_desc(n, S, P, H * R, cols), call
+
+
+def gma_state_store(state, codes, scales, src=None, dst=None, workspace=None, stream=None, check_status: bool = False):
+    """Put carried states away in 8 bits: state[src[i]] -> codes[dst[i]], scales[dst[i]] for every i.
+    state [S,H,R,C] float32 (the delta rule's [S,H,d,dv], gma_decode's [S,H,K,dv+1]), codes
+    [P,H,R,C] int8, scales [P,H,R,ceil(C/32)] float32, src and dst int32 [n] (default i).  Groups
+    of 32 along a row share a scale max|x| / 127.  A negative index marks an absent entry; one
+    outside its pool is skipped and posts GMA_ERR_BOUNDS; of several entries with one
+    destination the last counts.  Returns (codes, scales)."""
+    desc, call = _cache("gma_state_store", state, codes, scales, src, dst, stream, workspace)
+    call.run(_lib().gma_state_store, 256,
+             (ctypes.byref(desc),) + tuple(_ptr(t) for t in (state, src, dst, codes, scales)), check_status)
+    return codes, scales
+
+
+def gma_state_load(codes, scales, state, src=None, dst=None, workspace=None, stream=None, check_status: bool = False):
+    """Read states back from the 8-bit cache: codes[src[i]], scales[src[i]] -> state[dst[i]] for
+    every i (one source may go to many destinations).  Arguments as for gma_state_store.
+    Returns state."""
+    desc, call = _cache("gma_state_load", state, codes, scales, src, dst, stream, workspace)
+    call.run(_lib().gma_state_load, 256,
+             (ctypes.byref(desc),) + tuple(_ptr(t) for t in (codes, scales, src, dst, state)), check_status)
+    return state

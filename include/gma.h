@@ -53,7 +53,8 @@ typedef enum {
     GMA_ERR_WORKSPACE = 3,     /* workspace missing or smaller than required      */
     GMA_ERR_CUDA = 4,          /* a CUDA runtime call or kernel launch failed     */
     GMA_ERR_TIMEOUT = 5,       /* a device-side bounded wait ran out              */
-    GMA_ERR_BOUNDS = 6         /* a device-side index check failed (debug build)  */
+    GMA_ERR_BOUNDS = 6         /* a device-side index check failed: a slot or index given
+                                  to the decode or the state cache (or, debug build, any) */
 } gma_status;
 
 typedef enum { GMA_F32 = 0, GMA_BF16 = 1 } gma_dtype;
@@ -335,6 +336,93 @@ typedef struct {
 gma_status gma_project(const gma_proj_desc *desc, const void *X, const void *Wq, const void *Wk, const void *Wv,
                        void *Qx, void *Kx, void *V, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * The gated delta rule: the linear-time sequence mixer whose carried state is a
+ * [d, dv] matrix per head (the causal GMA's is [K, dv + 1]).  Per batch entry
+ * and value head h, with key head h / (H / Hk) and the state S (float32):
+ *   w_t = V_t - e^{g_t} S_{t-1}^T Kx_t
+ *   S_t = e^{g_t} S_{t-1} + Kx_t (beta_t w_t)^T
+ *   out_t = scale S_t^T Qx_t
+ * Layouts (row-major, contiguous, 16-byte aligned):
+ *   Qx, Kx [B, Hk, N, d], V, out [B, H, N, dv]    in_dtype
+ *   g, beta [B, H, N]                             gate_dtype
+ *   states [B, H, d, dv] (decode: [n_states, H, d, dv])    float32
+ *   lengths [B] int32 or NULL: rows at and past lengths[b] (held to [0, N]) do
+ *     not exist: their inputs are not used, out and every gradient is 0 there.
+ * d, dv from 1 to 256; H a multiple of Hk.  g is a log decay, normally <= 0;
+ * minus infinity or a very low value (below -1e5) forgets the state (a document
+ * boundary).  The recurrence is stable while beta |Kx|^2 <= 2.  beta = 0 with
+ * g = 0 leaves the state as it is.  A NaN or an infinity in a row may reach
+ * rows of the same 64-row chunk before it.
+ */
+typedef struct {
+    int B, H, Hk, N, d, dv;
+    gma_dtype in_dtype, gate_dtype;
+    float scale;
+} gma_delta_desc;
+
+/*
+ * A whole sequence.  state_in NULL: zeros.  state_out NULL: not wanted; it may
+ * be state_in.  N = 0 copies state_in to state_out.  With state_out every
+ * product that reaches the state carries fp32 values (three bf16 terms); without
+ * it two terms, as the bf16 output shows no more.
+ */
+gma_status gma_delta_workspace_size(const gma_delta_desc *desc, size_t *bytes);
+gma_status gma_delta_forward(const gma_delta_desc *desc, const void *Qx, const void *Kx, const void *V, const void *g,
+                             const void *beta, const int *lengths, const float *state_in, void *out, float *state_out,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradient: given dO [B, H, N, dv] (in_dtype) and, or NULL for zeros,
+ * dstate_out = dL/dS_N, writes dQx, dKx, dV (in_dtype; dQx and dKx summed over
+ * the value heads of a key head in order), dg, dbeta (gate_dtype) and, unless
+ * NULL, dstate_in = dL/dS_0 (float32; may be dstate_out).  Every output is
+ * overwritten.  No output may overlap an input otherwise.  Deterministic.
+ */
+gma_status gma_delta_backward_workspace_size(const gma_delta_desc *desc, size_t *bytes);
+gma_status gma_delta_backward(const gma_delta_desc *desc, const void *Qx, const void *Kx, const void *V, const void *g,
+                              const void *beta, const int *lengths, const float *state_in, const void *dO,
+                              const float *dstate_out, void *dQx, void *dKx, void *dV, void *dg, void *dbeta,
+                              float *dstate_in, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The next N positions (one, or a few) of sequences whose states lie in a pool
+ * [n_states, H, d, dv], read and updated in place in fp32.  slots [B] int32 or
+ * NULL (entry b at b, n_states >= B): the state of each batch entry.  A
+ * negative slot marks an entry that is not there (a padded batch): no state is
+ * touched and its out rows are 0.  A slot outside the pool, or one that an
+ * earlier entry already names, is treated the same and posts GMA_ERR_BOUNDS.
+ */
+gma_status gma_delta_decode_workspace_size(const gma_delta_desc *desc, size_t *bytes);
+gma_status gma_delta_decode(const gma_delta_desc *desc, const void *Qx, const void *Kx, const void *V, const void *g,
+                            const void *beta, const int *lengths, const int *slots, int n_states, float *state,
+                            void *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Carried states in an 8-bit cache (a parked session, the state after a shared
+ * prefix).  A state is `rows` rows (heads times the rows of a head) of `cols`
+ * float32 values: the delta rule's [H, d, dv] or gma_decode()'s [H, K, dv + 1].
+ * Each row is cut into groups of 32 from its start, the last one maybe shorter:
+ *   scale = max |x| / 127,  code = rint(x / scale)   (IEEE float32 divisions)
+ * and reads back as code * scale; the error is at most max |x| / 254.  A group
+ * that holds a NaN or an infinity reads back as NaN.
+ *   state  [n_states, rows, cols] float32     codes [n_cache, rows, cols] int8
+ *   scales [n_cache, rows, ceil(cols / 32)] float32
+ *   src, dst [n] int32 or NULL (entry i at i): where each state is read and
+ *   written.  A negative index marks an absent entry; an index outside its pool
+ *   is skipped and posts GMA_ERR_BOUNDS; of several entries with one
+ *   destination the last counts.  n up to 65535, rows * cols below 2^31.
+ * The workspace holds only the status word (256 bytes, zero at first).
+ */
+typedef struct {
+    int n, n_states, n_cache, rows, cols;
+} gma_state_desc;
+
+gma_status gma_state_store(const gma_state_desc *desc, const float *state, const int *src, const int *dst,
+                           signed char *codes, float *scales, void *workspace, size_t workspace_bytes, void *stream);
+gma_status gma_state_load(const gma_state_desc *desc, const signed char *codes, const float *scales, const int *src,
+                          const int *dst, float *state, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Size of the fixed scratch buffer gma_forward_noalloc() uses: 32 MiB. */
 #define GMA_NOALLOC_SCRATCH_BYTES ((size_t)32 << 20)
 
@@ -366,7 +454,8 @@ gma_status gma_forward_noalloc(const gma_desc *desc, const void *Qx, const void 
 /*
  * Synchronises `stream`, reads the device status word of `workspace`, clears
  * it, and returns GMA_OK or the device error that was posted: GMA_ERR_TIMEOUT,
- * or GMA_ERR_BOUNDS from a library built with GMA_DEBUG_BOUNDS defined, whose
+ * or GMA_ERR_BOUNDS from gma_delta_decode(), gma_state_store() or
+ * gma_state_load() for an index outside its pool, or from a library built with GMA_DEBUG_BOUNDS defined, whose
  * kernels check their global-memory indices (partial slots, heads, rows,
  * tiles) against the problem and skip, rather than perform, an access that
  * fails (a timeout is reported first when both were posted).

@@ -1,0 +1,76 @@
+"""The gated delta rule and the 8-bit state format in float64 numpy, row by row from their definitions."""
+import numpy as np
+
+
+def forward(Q, K, V, g, beta, scale, state=None, lengths=None, return_rows=False):
+    """Q, K [B,Hk,N,d], V [B,H,N,dv], g, beta [B,H,N] -> (out [B,H,N,dv], state [B,H,d,dv])."""
+    B, Hk, N, d = Q.shape
+    H, dv = V.shape[1], V.shape[3]
+    Q, K = (np.repeat(x.astype(np.float64), H // Hk, axis=1) for x in (Q, K))
+    V, g, beta = (x.astype(np.float64) for x in (V, g, beta))
+    S = np.zeros((B, H, d, dv)) if state is None else state.astype(np.float64).copy()
+    out = np.zeros((B, H, N, dv))
+    rows = []
+    for t in range(N):
+        live = np.ones(B, bool) if lengths is None else t < np.asarray(lengths)
+        k, q, v = (np.where(live[:, None, None], x[:, :, t], 0.0) for x in (K, Q, V))
+        a = np.where(live[:, None], np.exp(np.where(live[:, None], g[:, :, t], 0.0)), 1.0)
+        b = np.where(live[:, None], beta[:, :, t], 0.0)
+        before = S
+        faded = a[..., None, None] * S
+        w = v - np.einsum("bhkc,bhk->bhc", faded, k)
+        S = faded + k[..., None] * (b[..., None] * w)[:, :, None, :]
+        out[:, :, t] = scale * np.einsum("bhkc,bhk->bhc", S, q)
+        if return_rows:
+            rows.append((live, q, k, a, b, before, faded, w, S))
+    return (out, S, rows) if return_rows else (out, S)
+
+
+def backward(Q, K, V, g, beta, scale, dO, state=None, dstate=None, lengths=None):
+    """(dQ, dK, dV, dg, dbeta, dstate_in) by the reverse recurrence."""
+    B, Hk, N, d = Q.shape
+    H, dv = V.shape[1], V.shape[3]
+    rows = forward(Q, K, V, g, beta, scale, state, lengths, return_rows=True)[2]
+    R = np.zeros((B, H, d, dv)) if dstate is None else dstate.astype(np.float64).copy()
+    dQ, dK, dV = np.zeros((B, H, N, d)), np.zeros((B, H, N, d)), np.zeros((B, H, N, dv))
+    dg, db = np.zeros((B, H, N)), np.zeros((B, H, N))
+    for t in range(N - 1, -1, -1):
+        live, q, k, a, b, before, faded, w, after = rows[t]
+        do = np.where(live[:, None, None], dO[:, :, t].astype(np.float64), 0.0)
+        dQ[:, :, t] = scale * np.einsum("bhkc,bhc->bhk", after, do)
+        R = R + scale * q[..., None] * do[:, :, None, :]
+        du = np.einsum("bhkc,bhk->bhc", R, k)
+        db[:, :, t] = np.where(live[:, None], np.sum(du * w, -1), 0.0)
+        x = b[..., None] * du
+        dV[:, :, t] = x
+        dK[:, :, t] = np.einsum("bhkc,bhc->bhk", R, b[..., None] * w) - np.einsum("bhkc,bhc->bhk", faded, x)
+        R = R - k[..., None] * x[:, :, None, :]
+        dg[:, :, t] = np.where(live[:, None], a * np.sum(R * before, (-1, -2)), 0.0)
+        R = a[..., None, None] * R
+    r = H // Hk
+    dQ, dK = (x.reshape(B, Hk, r, N, d).sum(2) for x in (dQ, dK))
+    if lengths is not None:
+        dead = np.arange(N)[None, :] >= np.asarray(lengths)[:, None]
+        for x in (dQ, dK):
+            x[np.broadcast_to(dead[:, None, :], x.shape[:3])] = 0.0
+    return dQ, dK, dV, dg, db, R
+
+
+def quantise(x):
+    """x [..., cols] float32 -> (codes int8, scales float32 [..., ceil(cols / 32)]): float32 quotients, as the format says."""
+    cols = x.shape[-1]
+    groups = -(-cols // 32)
+    pad = np.zeros(x.shape[:-1] + (groups * 32,), np.float32)
+    pad[..., :cols] = x
+    y = pad.reshape(x.shape[:-1] + (groups, 32))
+    bad = ~np.isfinite(y).all(-1)
+    y = np.where(bad[..., None], np.float32(0), y)
+    scale = np.abs(y).max(-1) / np.float32(127)
+    with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
+        q = np.where(scale[..., None] > 0, y / scale[..., None], np.float32(0))
+    codes = np.clip(np.rint(q), -127, 127).astype(np.int8)
+    return codes.reshape(pad.shape)[..., :cols], np.where(bad, np.float32(np.nan), scale)
+
+
+def dequantise(codes, scales):
+    return codes.astype(np.float32) * np.repeat(scales, 32, axis=-1)[..., :codes.shape[-1]]
