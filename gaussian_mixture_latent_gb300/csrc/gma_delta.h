@@ -33,6 +33,12 @@ cudaError_t delta_rec_forward(const DeltaProblem &p, const DeltaRec &r, cudaStre
 // p.V is dO; state_in is dL/dS after the last row, state_out dL/dS before the first
 cudaError_t delta_rec_backward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s);
 
+// ----- chunks of 64 rows on the tensor cores, bf16: gma_delta_tc.cu -----
+constexpr int kTcRows = 64;
+bool delta_tc_supported(const DeltaProblem &p);
+cudaError_t delta_tc_forward(const DeltaProblem &p, const float *state_in, void *out, float *state_out,
+                             cudaStream_t s);
+
 struct DeltaGrads {
     const void *dO;
     const float *w, *du;              // [G, N, dv]
@@ -73,8 +79,9 @@ __device__ __forceinline__ int delta_len(const int *lengths, int b, int N) {
     return lengths ? min(max(lengths[b], 0), N) : N;
 }
 // A log decay at or below -1e5 forgets everything (e^g = 0 in fp32); holding it there keeps sums of a chunk's
-// decays finite, so that minus infinity and the type's lowest value are ordinary inputs.  NaN passes through.
-__device__ __forceinline__ float delta_floor(float g) { return g < -1e5f ? -1e5f : g; }
+// decays finite, so that minus infinity and the type's lowest value are ordinary inputs.  The same above (e^g is
+// infinite).  NaN passes through.
+__device__ __forceinline__ float delta_floor(float g) { return g < -1e5f ? -1e5f : g > 1e5f ? 1e5f : g; }
 #endif
 
 }  // namespace gma

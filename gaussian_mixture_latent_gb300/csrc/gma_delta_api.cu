@@ -44,6 +44,9 @@ bool all_aligned(const void *const (&ptrs)[M]) {
 
 gma_status launched(cudaError_t e) { return e == cudaSuccess ? GMA_OK : GMA_ERR_CUDA; }
 
+// Up to this many rows the row-by-row kernel is the faster one: it has no chunk to prepare.
+constexpr int kRecRows = 8;
+
 struct BwdLayout2 {
     size_t w, du, s0, ds, dq, dk, total;
 };
@@ -93,6 +96,8 @@ gma_status gma_delta_forward(const gma_delta_desc *desc, const void *Qx, const v
     if (!workspace || workspace_bytes < need) return GMA_ERR_WORKSPACE;
     if (desc->N == 0 && (!state_out || state_out == state_in)) return GMA_OK;
     const DeltaProblem p = problem(desc, Qx, Kx, V, g, beta, lengths, workspace);
+    if (delta_tc_supported(p) && desc->N > kRecRows)
+        return launched(delta_tc_forward(p, state_in, out, state_out, static_cast<cudaStream_t>(stream)));
     DeltaRec r{};
     r.state_in = state_in;
     r.state_out = state_out;

@@ -1,0 +1,148 @@
+// Device helpers of the chunked gated delta rule: register-resident tensor-core tiles (mma.sync m16n8k16, bf16
+// operands, fp32 accumulators), bf16 term splitting, ldmatrix / stmatrix, asynchronous copies.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+namespace gma {
+namespace dmma {
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void stsm_t(uint32_t at, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
+                 ::"r"(at), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+}
+
+// 16 bytes from global to shared memory, or zeros where there is nothing to read.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(dst), "l"(__cvta_generic_to_global(src)), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void bar(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory"); }
+
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float low(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float high(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+// A pair of fp32 values as NT packed bf16 terms, each the rounding of what the terms before it leave: two terms hold
+// 16 bits (2^-17 relative, half a step of the second), three all 24.
+template <int NT>
+__device__ __forceinline__ void split(float x, float y, uint32_t (&t)[NT]) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        t[i] = pack(x, y);
+        if (i + 1 < NT) {
+            x -= low(t[i]);
+            y -= high(t[i]);
+        }
+    }
+}
+
+// The A operand's terms (16 rows x 16 k) from two neighbouring accumulator tiles of 16 x 8.
+template <int NT>
+__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], uint32_t (&a)[NT][4]) {
+    uint32_t t[NT];
+    split<NT>(c0[0], c0[1], t);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) a[i][0] = t[i];
+    split<NT>(c0[2], c0[3], t);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) a[i][1] = t[i];
+    split<NT>(c1[0], c1[1], t);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) a[i][2] = t[i];
+    split<NT>(c1[2], c1[3], t);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) a[i][3] = t[i];
+}
+
+// Byte offset of 16-byte piece `c` of row `r` in a tile of ROWB-byte rows (32, 64, 128, 256): pieces are exchanged so
+// that eight rows of one piece column lie in eight different 16-byte columns of the 128-byte bank line.
+template <int ROWB>
+__device__ __forceinline__ uint32_t at(int r, int c) {
+    constexpr int per = ROWB >= 128 ? 1 : 128 / ROWB, mask = ROWB >= 128 ? 7 : ROWB / 16 - 1;
+    return r * ROWB + ((c ^ ((r / per) & mask)) << 4);
+}
+
+// A lower triangular 64 x 64 matrix in bf16 as its ten 16 x 16 blocks of 512 bytes.
+constexpr int kTriBytes = 10 * 512;
+__device__ __forceinline__ uint32_t tri(int ib, int jb) { return (ib * (ib + 1) / 2 + jb) * 512; }
+
+// fp32 tiles in shared memory whose products keep NT bf16 terms of each side (and the products that those terms reach).
+constexpr int kFp = 68;                               // row pitch in floats: the B operand's reads hit 32 banks
+template <int NT>
+__device__ __forceinline__ void frag_a32(const float *p, int pitch, int lane, uint32_t (&a)[NT][4]) {
+    const float *q = p + (lane >> 2) * pitch + 2 * (lane & 3);
+    const float2 x = *reinterpret_cast<const float2 *>(q), y = *reinterpret_cast<const float2 *>(q + 8 * pitch);
+    const float2 z = *reinterpret_cast<const float2 *>(q + 8), w = *reinterpret_cast<const float2 *>(q + 8 * pitch + 8);
+    const float c0[4] = {x.x, x.y, y.x, y.y}, c1[4] = {z.x, z.y, w.x, w.y};
+    split_a<NT>(c0, c1, a);
+}
+template <int NT>
+__device__ __forceinline__ void frag_b32(const float *p, int pitch, int lane, uint32_t (&b)[NT][2]) {
+    const float *q = p + 2 * (lane & 3) * pitch + (lane >> 2);
+    uint32_t t[NT];
+    split<NT>(q[0], q[pitch], t);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) b[i][0] = t[i];
+    split<NT>(q[8 * pitch], q[9 * pitch], t);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) b[i][1] = t[i];
+}
+template <int NT>
+__device__ __forceinline__ void mma32(float (&c)[4], const uint32_t (&a)[NT][4], const uint32_t (&b)[NT][2]) {
+#pragma unroll
+    for (int sum = NT - 1; sum >= 0; --sum)           // the smallest products first
+#pragma unroll
+        for (int i = 0; i <= sum; ++i) mma(c, a[i], b[sum - i][0], b[sum - i][1]);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Running sums of 64 base-2 log decays (two rows to a lane of one warp) as pairs of floats (hi + lo).  The sums are in
+// 32.32 fixed point: exact, so that a difference of two of them is good to 2^-32 however large they are (fp64 adds
+// would do, but cost 2000 cycles here).  A NaN decay makes its row and those after it NaN.
+__device__ __forceinline__ long long fixed_log2(float g) {
+    const float l2 = 1.44269502f, l2lo = 1.92596299e-8f;      // log2(e) in two floats
+    const float x = g * l2, y = fmaf(g, l2, -x) + g * l2lo;
+    return __float2ll_rn(x * 4294967296.f) + __float2ll_rn(y * 4294967296.f);
+}
+__device__ __forceinline__ float2 fixed_pair(long long q) {
+    const float hi = __ll2float_rn(q);
+    return make_float2(hi * 0x1p-32f, __ll2float_rn(q - __float2ll_rn(hi)) * 0x1p-32f);
+}
+
+}  // namespace dmma
+}  // namespace gma
