@@ -36,7 +36,8 @@ cudaError_t delta_rec_backward(const DeltaProblem &p, const DeltaRec &r, cudaStr
 // ----- chunks of 64 rows on the tensor cores, bf16: gma_delta_tc.cu -----
 constexpr int kTcRows = 64;
 bool delta_tc_supported(const DeltaProblem &p);
-cudaError_t delta_tc_forward(const DeltaProblem &p, const float *state_in, void *out, float *state_out,
+size_t delta_tc_workspace(const DeltaProblem &p);
+cudaError_t delta_tc_forward(const DeltaProblem &p, const float *state_in, void *out, float *state_out, char *ws,
                              cudaStream_t s);
 
 struct DeltaGrads {

@@ -46,6 +46,7 @@ gma_status launched(cudaError_t e) { return e == cudaSuccess ? GMA_OK : GMA_ERR_
 
 // Up to this many rows the row-by-row kernel is the faster one: it has no chunk to prepare.
 constexpr int kRecRows = 8;
+bool in_chunks(const DeltaProblem &p) { return delta_tc_supported(p) && p.N > kRecRows; }
 
 struct BwdLayout2 {
     size_t w, du, s0, ds, dq, dk, total;
@@ -80,7 +81,8 @@ gma_status gma_delta_workspace_size(const gma_delta_desc *desc, size_t *bytes) {
     const gma_status st = validate(desc);
     if (st != GMA_OK) return st;
     if (!bytes) return GMA_ERR_INVALID_ARG;
-    *bytes = kHeaderBytes;
+    const DeltaProblem p = problem(desc, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+    *bytes = kHeaderBytes + (in_chunks(p) ? delta_tc_workspace(p) : 0);
     return GMA_OK;
 }
 
@@ -96,8 +98,9 @@ gma_status gma_delta_forward(const gma_delta_desc *desc, const void *Qx, const v
     if (!workspace || workspace_bytes < need) return GMA_ERR_WORKSPACE;
     if (desc->N == 0 && (!state_out || state_out == state_in)) return GMA_OK;
     const DeltaProblem p = problem(desc, Qx, Kx, V, g, beta, lengths, workspace);
-    if (delta_tc_supported(p) && desc->N > kRecRows)
-        return launched(delta_tc_forward(p, state_in, out, state_out, static_cast<cudaStream_t>(stream)));
+    if (in_chunks(p))
+        return launched(delta_tc_forward(p, state_in, out, state_out, static_cast<char *>(workspace) + kHeaderBytes,
+                                         static_cast<cudaStream_t>(stream)));
     DeltaRec r{};
     r.state_in = state_in;
     r.state_out = state_out;

@@ -55,30 +55,49 @@ _scratch: dict = {}
 
 
 def _check(t, name, shape, dtypes, device):
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.is_contiguous()
+            and t.device == device and t.is_cuda):
+        return
     _gma._check(t, name, shape, dtypes)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 class _Call:
     """The device, stream and workspace of one call."""
 
     def __init__(self, what, device, stream, workspace):
-        if not isinstance(device, torch.device) or device.type != "cuda":
+        if device.type != "cuda":
             raise ValueError(f"{what}: tensors must be CUDA tensors")
         self.what, self.device, self.workspace = what, device, workspace
-        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
-        if self.stream.device != device:
-            raise ValueError(f"{what}: the stream is on {self.stream.device}, the tensors on {device}")
+        self.here = torch.cuda.current_device() == device.index
+        current = torch.cuda.current_stream(device)
+        self.stream = current if stream is None else stream
+        self.ptr = self.stream.cuda_stream
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
+            self.here = self.here and self.ptr == current.cuda_stream
+
+    def empty(self, shape, dtype):
+        """New memory on the call's device and stream."""
+        if self.here:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.device(self.device), torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
     def run(self, fn, need, args, check_status):
+        if self.here:
+            return self._run(fn, need, args, check_status)
         with torch.cuda.device(self.device), torch.cuda.stream(self.stream):
-            ws = self._workspace(need)
-            rc = fn(*args, ws.data_ptr(), ws.numel(), self.stream.cuda_stream)
-            if rc:
-                raise _gma.GmaError(rc, self.what)
-            if check_status:
-                _gma._check_device_status(ws, self.stream, self.what)
+            self._run(fn, need, args, check_status)
+
+    def _run(self, fn, need, args, check_status):
+        ws = self._workspace(need)
+        rc = fn(*args, ws.data_ptr(), ws.numel(), self.ptr)
+        if rc:
+            raise _gma.GmaError(rc, self.what)
+        if check_status:
+            _gma._check_device_status(ws, self.stream, self.what)
 
     def _workspace(self, need):
         ws = self.workspace
@@ -88,7 +107,7 @@ class _Call:
             if ws.numel() < need:
                 raise _gma.GmaError(3, self.what)
             return ws
-        key = (self.device.index, self.stream.cuda_stream)
+        key = (self.device.index, self.ptr)
         capturing = torch.cuda.is_current_stream_capturing()
         ws = None if capturing else _scratch.get(key)
         if ws is None or ws.numel() < need:
@@ -104,39 +123,42 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _sequence(what, Qx, Kx, V, g, beta, lengths, scale, stream, workspace):
-    """The checked description and call of one gated-delta-rule problem."""
-    for name, t, dims in (("Qx", Qx, 4), ("V", V, 4)):
+_plans: dict = {}
+
+
+def _sequence(what, size, Qx, Kx, V, g, beta, lengths, scale, stream, workspace):
+    """The checked description, workspace size and call of one gated-delta-rule problem."""
+    for name, t, dims in (("Qx", Qx, 4), ("V", V, 4), ("g", g, 3)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dim() != dims:
             raise ValueError(f"{name} has {t.dim()} dimensions, expected {dims}")
-    if not isinstance(g, torch.Tensor):
-        raise TypeError("g must be a torch.Tensor")
-    B, Hk, N, d = Qx.shape
+    B, Hk, N, d = keys = Qx.shape
     H, dv = V.shape[1], V.shape[3]
-    dev = Qx.device
+    dev, dt, gt = Qx.device, Qx.dtype, g.dtype
     call = _Call(what, dev, stream, workspace)
-    _check(Qx, "Qx", (B, Hk, N, d), _FLOATS, dev)
-    _check(Kx, "Kx", (B, Hk, N, d), (Qx.dtype,), dev)
-    _check(V, "V", (B, H, N, dv), (Qx.dtype,), dev)
+    _check(Qx, "Qx", keys, _FLOATS, dev)
+    _check(Kx, "Kx", keys, (dt,), dev)
+    _check(V, "V", (B, H, N, dv), (dt,), dev)
     _check(g, "g", (B, H, N), _FLOATS, dev)
-    _check(beta, "beta", (B, H, N), (g.dtype,), dev)
+    _check(beta, "beta", (B, H, N), (gt,), dev)
     if Hk == 0 or H % Hk:
         raise ValueError(f"V has {H} heads, expected a multiple of Qx's {Hk}")
     if lengths is not None:
         _check(lengths, "lengths", (B,), (torch.int32,), dev)
-    scale = d ** -0.5 if scale is None else float(scale)
-    desc = gma_delta_desc(B, H, Hk, N, d, dv, _gma._DTYPES[Qx.dtype], _gma._DTYPES[g.dtype], scale)
-    return desc, call
-
-
-def _need(fn, desc, what):
-    n = ctypes.c_size_t(0)
-    rc = fn(ctypes.byref(desc), ctypes.byref(n))
-    if rc:
-        raise _gma.GmaError(rc, what)
-    return n.value
+    key = (size, B, H, Hk, N, d, dv, dt, gt, scale)
+    plan = _plans.get(key)
+    if plan is None:
+        desc = gma_delta_desc(B, H, Hk, N, d, dv, _gma._DTYPES[dt], _gma._DTYPES[gt],
+                              d ** -0.5 if scale is None else float(scale))
+        n = ctypes.c_size_t(0)
+        rc = getattr(_lib(), size)(ctypes.byref(desc), ctypes.byref(n))
+        if rc:
+            raise _gma.GmaError(rc, what)
+        if len(_plans) > 4096:
+            _plans.clear()
+        plan = _plans[key] = (desc, n.value)
+    return plan + (call,)
 
 
 def gma_delta_forward(Qx, Kx, V, g, beta, state=None, lengths=None, scale=None, return_state: bool = False, out=None,
@@ -148,22 +170,22 @@ def gma_delta_forward(Qx, Kx, V, g, beta, state=None, lengths=None, scale=None, 
     `state` is the state before the first row (default zeros) and is not changed unless it is
     also state_out.  Rows at and past lengths[b] (int32 [B]) do not exist: out is 0 there.
     scale defaults to d ** -0.5."""
-    desc, call = _sequence("gma_delta_forward", Qx, Kx, V, g, beta, lengths, scale, stream, workspace)
-    lib = _lib()
-    need = _need(lib.gma_delta_workspace_size, desc, "gma_delta_forward")
-    shape = (desc.B, desc.H, desc.d, desc.dv)
-    with torch.cuda.device(call.device), torch.cuda.stream(call.stream):
-        if out is None:
-            out = torch.empty(V.shape, dtype=V.dtype, device=V.device)
-        if return_state and state_out is None:
-            state_out = torch.empty(shape, dtype=torch.float32, device=V.device)
-    _check(out, "out", tuple(V.shape), (V.dtype,), call.device)
-    for name, t in (("state", state), ("state_out", state_out)):
-        if t is not None:
-            _check(t, name, shape, (torch.float32,), call.device)
-    call.run(lib.gma_delta_forward, need,
-             (ctypes.byref(desc),) + tuple(_ptr(t) for t in (Qx, Kx, V, g, beta, lengths, state, out, state_out)),
-             check_status)
+    desc, need, call = _sequence("gma_delta_forward", "gma_delta_workspace_size", Qx, Kx, V, g, beta, lengths, scale,
+                                 stream, workspace)
+    shape = (V.shape[0], V.shape[1], Qx.shape[3], V.shape[3])
+    if out is None:
+        out = call.empty(V.shape, V.dtype)
+    else:
+        _check(out, "out", V.shape, (V.dtype,), call.device)
+    if state is not None:
+        _check(state, "state", shape, (torch.float32,), call.device)
+    if state_out is not None:
+        _check(state_out, "state_out", shape, (torch.float32,), call.device)
+    elif return_state:
+        state_out = call.empty(shape, torch.float32)
+    call.run(_lib().gma_delta_forward, need,
+             (ctypes.byref(desc), Qx.data_ptr(), Kx.data_ptr(), V.data_ptr(), g.data_ptr(), beta.data_ptr(),
+              _ptr(lengths), _ptr(state), out.data_ptr(), _ptr(state_out)), check_status)
     return out if state_out is None else (out, state_out)
 
 
@@ -173,23 +195,22 @@ def gma_delta_backward(Qx, Kx, V, g, beta, dO, state=None, dstate=None, lengths=
     returned state was used, dstate = dL/dstate [B,H,d,dv] float32, returns (dQx, dKx, dV, dg, dbeta,
     dstate_in), each in its input's type; dstate_in (float32) is None when `state` is None.
     `grads`, if given, is that tuple of preallocated outputs (overwritten)."""
-    desc, call = _sequence("gma_delta_backward", Qx, Kx, V, g, beta, lengths, scale, stream, workspace)
-    lib = _lib()
-    _check(dO, "dO", tuple(V.shape), (V.dtype,), call.device)
+    desc, need, call = _sequence("gma_delta_backward", "gma_delta_backward_workspace_size", Qx, Kx, V, g, beta, lengths,
+                                 scale, stream, workspace)
+    _check(dO, "dO", V.shape, (V.dtype,), call.device)
     shape = (desc.B, desc.H, desc.d, desc.dv)
     for name, t in (("state", state), ("dstate", dstate)):
         if t is not None:
             _check(t, name, shape, (torch.float32,), call.device)
-    need = _need(lib.gma_delta_backward_workspace_size, desc, "gma_delta_backward")
+    inputs = (Qx, Kx, V, g, beta, state)
     if grads is None:
-        with torch.cuda.device(call.device), torch.cuda.stream(call.stream):
-            grads = tuple(torch.empty_like(t) for t in (Qx, Kx, V, g, beta)) + (
-                None if state is None else torch.empty_like(state),)
-    for t, like, name in zip(grads, (Qx, Kx, V, g, beta, state), ("dQx", "dKx", "dV", "dg", "dbeta", "dstate_in")):
-        if like is not None:
-            _check(t, name, tuple(like.shape), (like.dtype,), call.device)
+        grads = tuple(None if t is None else call.empty(t.shape, t.dtype) for t in inputs)
+    else:
+        for t, like, name in zip(grads, inputs, ("dQx", "dKx", "dV", "dg", "dbeta", "dstate_in")):
+            if like is not None:
+                _check(t, name, like.shape, (like.dtype,), call.device)
     dstate_in = grads[5] if state is not None else None
-    call.run(lib.gma_delta_backward, need,
+    call.run(_lib().gma_delta_backward, need,
              (ctypes.byref(desc),) + tuple(_ptr(t) for t in (Qx, Kx, V, g, beta, lengths, state, dO, dstate) +
                                            tuple(grads[:5]) + (dstate_in,)), check_status)
     return tuple(grads[:5]) + (dstate_in,)
@@ -202,23 +223,23 @@ def gma_delta_decode(Qx, Kx, V, g, beta, state, slots=None, lengths=None, scale=
     state[b]).  A negative slot marks an absent entry: its out rows are 0.  A slot outside the
     pool, or one that an earlier entry names, is treated so too and posts GMA_ERR_BOUNDS
     (raised with check_status).  Returns out [B,H,N,dv]."""
-    desc, call = _sequence("gma_delta_decode", Qx, Kx, V, g, beta, lengths, scale, stream, workspace)
-    lib = _lib()
-    need = _need(lib.gma_delta_decode_workspace_size, desc, "gma_delta_decode")
+    desc, need, call = _sequence("gma_delta_decode", "gma_delta_decode_workspace_size", Qx, Kx, V, g, beta, lengths,
+                                 scale, stream, workspace)
     if not isinstance(state, torch.Tensor):
         raise TypeError("state must be a torch.Tensor")
     if state.dim() != 4:
         raise ValueError(f"state has {state.dim()} dimensions, expected 4")
-    _check(state, "state", (state.shape[0], desc.H, desc.d, desc.dv), (torch.float32,), call.device)
+    pool = state.shape[0]
+    _check(state, "state", (pool, V.shape[1], Qx.shape[3], V.shape[3]), (torch.float32,), call.device)
     if slots is not None:
-        _check(slots, "slots", (desc.B,), (torch.int32,), call.device)
+        _check(slots, "slots", (V.shape[0],), (torch.int32,), call.device)
     if out is None:
-        with torch.cuda.device(call.device), torch.cuda.stream(call.stream):
-            out = torch.empty(V.shape, dtype=V.dtype, device=V.device)
-    _check(out, "out", tuple(V.shape), (V.dtype,), call.device)
-    call.run(lib.gma_delta_decode, need,
-             (ctypes.byref(desc),) + tuple(_ptr(t) for t in (Qx, Kx, V, g, beta, lengths, slots)) +
-             (state.shape[0], _ptr(state), _ptr(out)), check_status)
+        out = call.empty(V.shape, V.dtype)
+    else:
+        _check(out, "out", V.shape, (V.dtype,), call.device)
+    call.run(_lib().gma_delta_decode, need,
+             (ctypes.byref(desc), Qx.data_ptr(), Kx.data_ptr(), V.data_ptr(), g.data_ptr(), beta.data_ptr(),
+              _ptr(lengths), _ptr(slots), pool, state.data_ptr(), out.data_ptr()), check_status)
     return out
 
 
@@ -254,7 +275,8 @@ def gma_state_store(state, codes, scales, src=None, dst=None, workspace=None, st
     destination the last counts.  Returns (codes, scales)."""
     desc, call = _cache("gma_state_store", state, codes, scales, src, dst, stream, workspace)
     call.run(_lib().gma_state_store, 256,
-             (ctypes.byref(desc),) + tuple(_ptr(t) for t in (state, src, dst, codes, scales)), check_status)
+             (ctypes.byref(desc), state.data_ptr(), _ptr(src), _ptr(dst), codes.data_ptr(), scales.data_ptr()),
+             check_status)
     return codes, scales
 
 
@@ -264,5 +286,6 @@ def gma_state_load(codes, scales, state, src=None, dst=None, workspace=None, str
     Returns state."""
     desc, call = _cache("gma_state_load", state, codes, scales, src, dst, stream, workspace)
     call.run(_lib().gma_state_load, 256,
-             (ctypes.byref(desc),) + tuple(_ptr(t) for t in (codes, scales, src, dst, state)), check_status)
+             (ctypes.byref(desc), codes.data_ptr(), scales.data_ptr(), _ptr(src), _ptr(dst), state.data_ptr()),
+             check_status)
     return state
