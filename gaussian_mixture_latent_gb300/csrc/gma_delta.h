@@ -40,6 +40,21 @@ size_t delta_tc_workspace(const DeltaProblem &p);
 cudaError_t delta_tc_forward(const DeltaProblem &p, const float *state_in, void *out, float *state_out, char *ws,
                              cudaStream_t s);
 
+// The gradient in chunks: prep, the chain with checkpoints, the reverse chain, the gradients (gma_delta_grads.cu).
+struct DeltaTcGrads {
+    const void *dO;
+    const char *chunks;
+    const float *w, *x;               // [G, N, dv]
+    const __nv_bfloat16 *s0, *ds;     // [G, nc, dv, d]: S before, dL/dS after each chunk
+    float *dq_heads, *dk_heads;       // [G, N, d] per value head; null when H == Hk
+    void *dQ, *dK, *dV, *dg, *dbeta;
+};
+cudaError_t delta_tc_grads(const DeltaProblem &p, const DeltaTcGrads &g, int chunk_bytes, int vec_at, cudaStream_t s);
+size_t delta_tc_backward_workspace(const DeltaProblem &p);
+cudaError_t delta_tc_backward(const DeltaProblem &p, const float *state_in, const void *dO, const float *dstate_out,
+                              void *dQ, void *dK, void *dV, void *dg, void *dbeta, float *dstate_in, char *ws,
+                              cudaStream_t s);
+
 struct DeltaGrads {
     const void *dO;
     const float *w, *du;              // [G, N, dv]

@@ -48,14 +48,14 @@ gma_status launched(cudaError_t e) { return e == cudaSuccess ? GMA_OK : GMA_ERR_
 constexpr int kRecRows = 8;
 bool in_chunks(const DeltaProblem &p) { return delta_tc_supported(p) && p.N > kRecRows; }
 
-struct BwdLayout2 {
+struct RecLayout {
     size_t w, du, s0, ds, dq, dk, total;
 };
 
-BwdLayout2 backward_layout(const gma_delta_desc *d) {
+RecLayout backward_layout(const gma_delta_desc *d) {
     const size_t G = (size_t)d->B * d->H, rows = G * d->N;
     const size_t nchunk = ((size_t)d->N + kRecChunk - 1) / kRecChunk;
-    BwdLayout2 L{};
+    RecLayout L{};
     size_t o = kHeaderBytes;
     auto take = [&](size_t floats) { const size_t at = o; o += align_up(floats * sizeof(float)); return at; };
     L.w = take(rows * d->dv);
@@ -140,7 +140,8 @@ gma_status gma_delta_backward_workspace_size(const gma_delta_desc *desc, size_t 
     const gma_status st = validate(desc);
     if (st != GMA_OK) return st;
     if (!bytes) return GMA_ERR_INVALID_ARG;
-    *bytes = backward_layout(desc).total;
+    const DeltaProblem p = problem(desc, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+    *bytes = in_chunks(p) ? kHeaderBytes + delta_tc_backward_workspace(p) : backward_layout(desc).total;
     return GMA_OK;
 }
 
@@ -155,14 +156,18 @@ gma_status gma_delta_backward(const gma_delta_desc *desc, const void *Qx, const 
     const void *const ptrs[] = {Qx, Kx, V, g, beta, lengths, state_in, dO, dstate_out, dQx, dKx, dV, dg, dbeta,
                                 dstate_in, workspace};
     if (!all_aligned(ptrs)) return GMA_ERR_INVALID_ARG;
-    const BwdLayout2 L = backward_layout(desc);
-    if (!workspace || workspace_bytes < L.total) return GMA_ERR_WORKSPACE;
+    size_t need = 0;
+    gma_delta_backward_workspace_size(desc, &need);
+    if (!workspace || workspace_bytes < need) return GMA_ERR_WORKSPACE;
     if (desc->N == 0 && (!dstate_in || dstate_in == dstate_out)) return GMA_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
     auto at = [&](size_t o) { return reinterpret_cast<float *>(ws + o); };
-    DeltaProblem p = problem(desc, Qx, Kx, V, g, beta, lengths, workspace);
-
+    const DeltaProblem p = problem(desc, Qx, Kx, V, g, beta, lengths, workspace);
+    if (in_chunks(p))
+        return launched(delta_tc_backward(p, state_in, dO, dstate_out, dQx, dKx, dV, dg, dbeta, dstate_in,
+                                          ws + kHeaderBytes, s));
+    const RecLayout L = backward_layout(desc);
     cudaError_t e;
     if (desc->N > 0) {
         // the states before each chunk and w of each row; its O goes where dV will be written

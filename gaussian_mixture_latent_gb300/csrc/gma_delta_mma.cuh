@@ -6,6 +6,8 @@
 
 #include <cstdint>
 
+#include "gma_delta.h"
+
 namespace gma {
 namespace dmma {
 
@@ -143,6 +145,21 @@ __device__ __forceinline__ float2 fixed_pair(long long q) {
     const float hi = __ll2float_rn(q);
     return make_float2(hi * 0x1p-32f, __ll2float_rn(q - __float2ll_rn(hi)) * 0x1p-32f);
 }
+
+template <int V>
+struct Int { static constexpr int value = V; };
+
+struct Vec {                           // one chunk's row factors
+    float2 G[kTcRows];                       // running sum of the log2 decays, hi + lo
+    float e[kTcRows], f[kTcRows], beta[kTcRows];         // e^G, e^{G_C - G}
+    float last, pad[3];                // e^{G_C}
+};
+// One chunk in the workspace: T's NT terms and P's two, as packed triangles, then the factors.
+template <int NT>
+struct Chunk {
+    static constexpr int oP = NT * kTriBytes, oVec = oP + 2 * kTriBytes, bytes = oVec + (int)sizeof(Vec);
+    static_assert(bytes % 16 == 0, "copied in pieces of 16 bytes");
+};
 
 }  // namespace dmma
 }  // namespace gma

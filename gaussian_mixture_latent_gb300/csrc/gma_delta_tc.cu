@@ -24,21 +24,6 @@ using namespace dmma;
 
 constexpr int C = kTcRows;
 
-template <int V>
-struct Int { static constexpr int value = V; };
-
-struct Vec {                           // one chunk's row factors
-    float2 G[C];                       // running sum of the log2 decays, hi + lo
-    float e[C], f[C], beta[C];         // e^G, e^{G_C - G}
-    float last, pad[3];                // e^{G_C}
-};
-// One chunk in the workspace: T's NT terms and P's two, as packed triangles, then the factors.
-template <int NT>
-struct Chunk {
-    static constexpr int oP = NT * kTriBytes, oVec = oP + 2 * kTriBytes, bytes = oVec + (int)sizeof(Vec);
-    static_assert(bytes % 16 == 0, "copied in pieces of 16 bytes");
-};
-
 // -------------------------------------------------------------------------------------------------- delta_prep
 // One CTA of eight warps to a chunk.  Warps 0-3 take a row block of K K^T each and the inverse, warps 4-7 Q K^T.
 // T is inverted in fp32: 16 x 16 diagonal blocks by substitution (a product of powers would overflow for repeated
@@ -271,50 +256,57 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(const PrepA
 //   (K S)^T = S^T K^T,  U^T = R^T T^T,  O^T = S^T Q^T + U^T P^T,  S^T += (f U)^T K,
 // and an accumulator tile is the next product's A operand as it stands.  The right sides (K, Q, T, P) are read from
 // shared memory with ldmatrix; four loader warps copy chunk c + kStages - 1 while chunk c is worked on.
-// The KS warps split the first product's sum (their parts of d), then the 64 rows (eight-row tiles r, 7 - r, ..: the
+// KS > 1: the warps split the first product's sum (their parts of d), then the 64 rows (eight-row tiles r, 7 - r, ..: the
 // same work under the triangles), then the columns of S^T; in between they exchange partial sums, R and U through shared
 // memory, lane by lane.
 //
-// Checkpoint form (for the backward): no O; writes S before each chunk and W = U / beta, with |beta| held to at least
-// 2^-64 (a beta of 0 then adds 2^-64 W to the state, nothing in fp32).
+// kCkpt (for the backward): no O; writes S before each chunk (bf16, [dv, d]) and W = U / beta, with |beta| held to at
+// least 2^-64 (a beta of 0 then adds 2^-64 W to the state, nothing in fp32).
+// kBack: the reverse recurrence, with the state R = dL/dS [d, dv] after the chunk:
+//   dU = P^T dO + diag(f) K R,  X = T^T dU,  R <- e^{G_C} R + (scale diag(e^G) Q)^T dO - (diag(e^G beta) K)^T X,
+// the same chain with the triangles transposed; writes R after each chunk and X.
 //
 // Bound by the chain: mma.sync issues one m16n8k16 each 8.0 cycles on each of the SM's four tensor units (measured,
 // 1 to 16 warps; latency 21), and the products of a chunk depend on one another.  tcgen05 has four times that rate,
 // but its accumulators are in TMEM: three dependent products a chunk would each pay a round trip (load, split, store,
 // fence, issue) of about a chunk's time here.
-constexpr int kChainThreads = 256, kLoadThreads = 128, kAllThreads = kChainThreads + kLoadThreads;
-// Registers: the block is launched with 168 a thread (384 x 168 = 64512); 256 x 232 + 128 x 40 = 64512.
-constexpr int kChainRegs = 232, kLoadRegs = 40;
+enum Mode { kFwd, kCkpt, kBack };
+constexpr int kLoadThreads = 128;
+constexpr int kLoadRegs = 40;
 enum { kBarAll = 1, kBarSlice = 2 };   // named barriers; the slices use 2..5
 
 struct ChainArgs {
-    DeltaProblem p;
+    DeltaProblem p;                    // kBack: V is dO
     const char *chunks;
     int nc, groups;                    // chunks of a head; CTAs of a head
-    const float *state_in;
-    float *state_out;
-    void *out;
-    float *w;                          // checkpoint form: [G, N, dv]
-    __nv_bfloat16 *s0;                 // checkpoint form: [G, nc, dv, d], S before each chunk
+    const float *state_in;             // kBack: dL/dS after the last row
+    float *state_out;                  // kBack: dL/dS before the first
+    void *out;                         // kFwd
+    float *rows;                       // kCkpt: W, kBack: X, [G, N, dv]
+    __nv_bfloat16 *states;             // kCkpt: S before, kBack: R after each chunk, [G, nc, dv, d]
 };
 
-template <int D, int NT, int SL>
+template <int D, int NT, int SL, int KS>
 struct ChainSmem {
-    static constexpr int KS = 8 / SL;
+    static constexpr int kThreads = 32 * SL * KS, kAll = kThreads + kLoadThreads;
+    // Registers.  Eight chain warps: launched with 168 a thread, 384 x 168 = 64512 = 256 x 232 + 128 x 40.  Fewer need no split.
+    static constexpr bool kSplit = kThreads == 256;
+    static constexpr int kChainRegs = 232;
     static constexpr int kRow = 2 * D, kKey = C * kRow, kValRow = 32 * SL, kVal = C * kValRow;
     static constexpr int oQ = kKey, oV = 2 * kKey, oW = oV + kVal, kStage = oW + Chunk<NT>::bytes;
-    static constexpr int kSum = KS * 4096, kRows = 2048 * (NT > 2 ? NT : 2);    // of one slice
+    static constexpr int kSum = KS > 1 ? KS * 4096 : 0, kRows = KS > 1 ? 2048 * (NT > 2 ? NT : 2) : 0;    // of one slice
     static constexpr int kShared = SL * (kSum + kRows);
     static constexpr int kStages = 3 * kStage + kShared <= 227 * 1024 ? 3 : 2;
     static constexpr int oSum = kStages * kStage, oRows = oSum + SL * kSum, total = oRows + SL * kRows;
     static_assert(total <= 227 * 1024, "shared memory");
 };
 
-template <int D, int NT, int SL, bool CKPT>
-__global__ void __launch_bounds__(kAllThreads, 1) delta_chain_kernel(const ChainArgs a) {
-    using L = ChainSmem<D, NT, SL>;
+template <int D, int NT, int SL, int KS, int MODE>
+__global__ void __launch_bounds__(32 * SL * KS + kLoadThreads, 1) delta_chain_kernel(const ChainArgs a) {
+    using L = ChainSmem<D, NT, SL, KS>;
     using W = Chunk<NT>;
-    constexpr int KS = L::KS, DK = D / KS, OWN = 8 / KS;
+    constexpr int DK = D / KS, OWN = 8 / KS, kAll = L::kAll;
+    constexpr bool BACK = MODE == kBack;
     extern __shared__ __align__(128) char sm[];
     const uint32_t sb = smem_u32(sm);
     const DeltaProblem &p = a.p;
@@ -327,20 +319,21 @@ __global__ void __launch_bounds__(kAllThreads, 1) delta_chain_kernel(const Chain
     const size_t vrow = (size_t)bh * p.N, krow = ((size_t)b * p.Hk + hk) * p.N;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
 
-    if (tid >= kChainThreads) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-        const int lt = tid - kChainThreads;
+    if (tid >= L::kThreads) {
+        if (L::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+        const int lt = tid - L::kThreads;
         const __nv_bfloat16 *K = static_cast<const __nv_bfloat16 *>(p.Kx), *Q = static_cast<const __nv_bfloat16 *>(p.Qx);
         const __nv_bfloat16 *V = static_cast<const __nv_bfloat16 *>(p.V);
-        auto load = [&](int c) {
-            if (c < nc) {
-                const uint32_t st = sb + (c % L::kStages) * L::kStage;
+        auto load = [&](int i_th) {
+            if (i_th < nc) {
+                const int c = BACK ? nc - 1 - i_th : i_th;
+                const uint32_t st = sb + (i_th % L::kStages) * L::kStage;
                 for (int i = lt; i < C * (D / 8); i += kLoadThreads) {
                     const int r = i / (D / 8), col = i % (D / 8), row = c * C + r;
                     const bool ok = row < len && col * 8 < p.d;
                     const size_t off = ok ? (krow + row) * p.d + col * 8 : 0;
                     copy16(st + at<L::kRow>(r, col), K + off, ok);
-                    if (!CKPT) copy16(st + L::oQ + at<L::kRow>(r, col), Q + off, ok);
+                    if (MODE != kCkpt) copy16(st + L::oQ + at<L::kRow>(r, col), Q + off, ok);
                 }
                 for (int i = lt; i < C * 2 * SL; i += kLoadThreads) {
                     const int r = i / (2 * SL), col = i % (2 * SL), row = c * C + r;
@@ -355,22 +348,22 @@ __global__ void __launch_bounds__(kAllThreads, 1) delta_chain_kernel(const Chain
         };
         for (int c = 0; c < L::kStages - 1; ++c) load(c);
         copy_wait<L::kStages - 2>();
-        bar<kAllThreads>(kBarAll);
+        bar<kAll>(kBarAll);
         for (int c = 0; c < nc; ++c) {
             load(c + L::kStages - 1);
             copy_wait<L::kStages - 2>();
-            bar<kAllThreads>(kBarAll);
+            bar<kAll>(kBarAll);
         }
         copy_wait<0>();
-        if (!CKPT) {                                     // rows that do not exist
+        if (MODE == kFwd) {                              // rows that do not exist
             const int w = min(16 * SL, p.dv - c0) / 8;
             for (size_t i = lt; i < (size_t)(p.N - len) * w; i += kLoadThreads)
                 *reinterpret_cast<uint4 *>(out + (vrow + len + i / w) * p.dv + c0 + (int)(i % w) * 8) = make_uint4(0, 0, 0, 0);
         }
         return;
     }
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChainRegs));
-    const int slice = warp % SL, rank = warp / SL;
+    if (L::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kChainRegs));
+    const int slice = warp % SL, rank = KS > 1 ? warp / SL : 0;
     const int col = c0 + 16 * slice + (lane >> 2), q0 = 2 * (lane & 3), k0 = rank * DK;
     const size_t sbase = (size_t)bh * p.d * p.dv;
     float S[DK / 8][4];                                  // S^T: rows col, col + 8; columns k0 + 8 n + q0, + 1
@@ -383,71 +376,148 @@ __global__ void __launch_bounds__(kAllThreads, 1) delta_chain_kernel(const Chain
         }
     const int br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;              // B operand: rows n, pieces k
     const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, tc = lane >> 4;              // transposed: rows k, pieces n
-    // the warp's eight-row tiles: r, 7 - r (and r + 2, 5 - r of two warps)
-    auto own = [&](int j) { return j == 0 ? rank : j == 1 ? 7 - rank : j == 2 ? rank + 2 : 5 - rank; };
+    // the warp's eight-row tiles: all, or r, 7 - r (and r + 2, 5 - r of two warps)
+    auto own = [&](int j) {
+        return KS == 1 ? j : j == 0 ? rank : j == 1 ? 7 - rank : j == 2 ? rank + 2 : 5 - rank;
+    };
     float4 *sums = reinterpret_cast<float4 *>(sm + L::oSum + slice * L::kSum);      // [KS][8 tiles][32 lanes]
     char *rows = sm + L::oRows + slice * L::kRows;
+    auto meet = [&] { if (KS > 1) bar<32 * KS>(kBarSlice + slice); };
     auto put_sums = [&](const float (&x)[8][4]) {
+        if (KS > 1)
 #pragma unroll
-        for (int n = 0; n < 8; ++n) sums[(rank * 8 + n) * 32 + lane] = make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
+            for (int n = 0; n < 8; ++n) sums[(rank * 8 + n) * 32 + lane] = make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
     };
-    auto get_sum = [&](int n, float (&x)[4]) {
-        float4 y = sums[n * 32 + lane];
+    auto get_sums = [&](const float (&all)[8][4], float (&x)[OWN][4]) {
 #pragma unroll
-        for (int k = 1; k < KS; ++k) {
-            const float4 z = sums[(k * 8 + n) * 32 + lane];
-            y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+        for (int j = 0; j < OWN; ++j) {
+            if (KS == 1) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) x[j][m] = all[j][m];
+            } else {
+                const int n = own(j);
+                float4 y = sums[n * 32 + lane];
+#pragma unroll
+                for (int k = 1; k < KS; ++k) {
+                    const float4 z = sums[(k * 8 + n) * 32 + lane];
+                    y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+                }
+                x[j][0] = y.x; x[j][1] = y.y; x[j][2] = y.z; x[j][3] = y.w;
+            }
         }
-        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
     };
-    // x[j] += (rows of F^T) (triangle)^T for the warp's tiles: FT terms of F, TT of the triangle, the products that matter
+    // the A operand's terms of all 64 rows from each warp's tiles
+    auto offer_terms = [&](const float (&x)[OWN][4]) {
+        if (KS > 1)
+#pragma unroll
+            for (int j = 0; j < OWN; ++j) {
+                uint32_t t0[NT], t1[NT];
+                split<NT>(x[j][0], x[j][1], t0);
+                split<NT>(x[j][2], x[j][3], t1);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    reinterpret_cast<uint2 *>(rows)[(t * 8 + own(j)) * 32 + lane] = make_uint2(t0[t], t1[t]);
+            }
+    };
+    auto take_terms = [&](const float (&x)[OWN][4], uint32_t (&f)[4][NT][4]) {
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+            if (KS == 1) {
+                split_a<NT>(x[(2 * kb) % OWN], x[(2 * kb + 1) % OWN], f[kb]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint2 u0 = reinterpret_cast<const uint2 *>(rows)[(t * 8 + 2 * kb) * 32 + lane];
+                    const uint2 u1 = reinterpret_cast<const uint2 *>(rows)[(t * 8 + 2 * kb + 1) * 32 + lane];
+                    f[kb][t][0] = u0.x; f[kb][t][1] = u0.y; f[kb][t][2] = u1.x; f[kb][t][3] = u1.y;
+                }
+            }
+        }
+    };
+    auto share = [&](const float (&x)[OWN][4], float (&z)[8][4]) {
+        if (KS > 1) {
+#pragma unroll
+            for (int j = 0; j < OWN; ++j)
+                reinterpret_cast<float4 *>(rows)[own(j) * 32 + lane] = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
+            meet();
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            float4 y;
+            if (KS == 1) y = make_float4(x[n % OWN][0], x[n % OWN][1], x[n % OWN][2], x[n % OWN][3]);
+            else y = reinterpret_cast<const float4 *>(rows)[n * 32 + lane];
+            z[n][0] = y.x; z[n][1] = y.y; z[n][2] = y.z; z[n][3] = y.w;
+        }
+    };
+    // x += F^T M^T (BACK: F^T M) for the warp's tiles, M a packed triangle: FT terms of F, TT of M, their products up to
+    // MOST in the terms' sum
     auto triangle = [&](auto &x, const auto &f, uint32_t t0, auto ft, auto tt, auto most) {
         constexpr int FT = decltype(ft)::value, TT = decltype(tt)::value, MOST = decltype(most)::value;
 #pragma unroll
         for (int j = 0; j < OWN; ++j) {
-            const int n = own(j), ib = n >> 1;
+            const int n = own(j), nb = n >> 1;
 #pragma unroll
-            for (int jb = 0; jb < 4; jb += 2) {
-                if (jb > ib) continue;
-                // two blocks of the row at a time (the second one is the first again past the diagonal)
-                const uint32_t blk = t0 + tri(ib, min(jb + (lane >> 4), ib)) + at<32>((n & 1) * 8 + (lane & 7), bc);
+            for (int kb = 0; kb < 4; kb += 2) {
+                // blocks kb and kb + 1 along the sum; one outside the triangle is read as its neighbour and not used
+                const bool one = BACK ? kb >= nb : kb <= nb, two = BACK ? kb + 1 >= nb : kb + 1 <= nb;
+                if (!one && !two) continue;
+                const int k = kb + (lane >> 4);
+                const uint32_t blk = t0 + (BACK ? tri(max(k, nb), nb) + at<32>(lane & 15, n & 1)
+                                                : tri(nb, min(k, nb)) + at<32>((n & 1) * 8 + (lane & 7), bc));
 #pragma unroll
                 for (int t = TT - 1; t >= 0; --t) {
                     uint32_t fb[4];
-                    ldsm(fb, blk + t * kTriBytes);
+                    if (BACK) ldsm_t(fb, blk + t * kTriBytes);
+                    else ldsm(fb, blk + t * kTriBytes);
 #pragma unroll
                     for (int s = FT - 1; s >= 0; --s) {
                         if (s + t > MOST) continue;
-                        mma(x[j], f[jb][s], fb[0], fb[1]);
-                        if (jb + 1 <= ib) mma(x[j], f[jb + 1][s], fb[2], fb[3]);
+                        if (one) mma(x[j], f[kb][s], fb[0], fb[1]);
+                        if (two) mma(x[j], f[kb + 1][s], fb[2], fb[3]);
                     }
                 }
             }
         }
     };
-    bar<kAllThreads>(kBarAll);
-    for (int c = 0; c < nc; ++c) {
-        char *st = sm + (c % L::kStages) * L::kStage;
+    // S += Z^T B for the warp's columns, Z in NT terms, B the rows of a tile
+    auto add_outer = [&](const float (&z0)[4], const float (&z1)[4], int kb, uint32_t tile) {
+        uint32_t fs[NT][4];
+        split_a<NT>(z0, z1, fs);
+#pragma unroll
+        for (int nd = 0; nd < DK / 16; ++nd) {
+            uint32_t fb[4];
+            ldsm_t(fb, tile + at<L::kRow>(kb * 16 + tr, k0 / 8 + 2 * nd + tc));
+#pragma unroll
+            for (int t = NT - 1; t >= 0; --t) {
+                mma(S[2 * nd], fs[t], fb[0], fb[1]);
+                mma(S[2 * nd + 1], fs[t], fb[2], fb[3]);
+            }
+        }
+    };
+    bar<kAll>(kBarAll);
+    for (int ci = 0; ci < nc; ++ci) {
+        const int c = BACK ? nc - 1 - ci : ci;
+        char *st = sm + (ci % L::kStages) * L::kStage;
         const uint32_t kt = smem_u32(st), qt = kt + L::oQ, vt = kt + L::oV, tt = kt + L::oW, pt = tt + W::oP;
         const Vec &vec = *reinterpret_cast<const Vec *>(st + L::oW + W::oVec);
-        if (CKPT) {
-            // S^T as it is held: [dv, d] in bf16
+        if (MODE != kFwd) {
+            // the state as it is held: [dv, d] in bf16
 #pragma unroll
             for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int r = k0 + 8 * n + q0, cc = col + 8 * j;
                     if (r < p.d && cc < p.dv)
-                        *reinterpret_cast<uint32_t *>(a.s0 + (((size_t)bh * a.nc + c) * p.dv + cc) * p.d + r) =
+                        *reinterpret_cast<uint32_t *>(a.states + (((size_t)bh * a.nc + c) * p.dv + cc) * p.d + r) =
                             pack(S[n][2 * j], S[n][2 * j + 1]);
                 }
         }
+        // y = (K S)^T in NT terms of S; kFwd: o = (Q S)^T in one.  This warp's part of the sum over d.
         float y[8][4], o[8][4];
 #pragma unroll
         for (int n = 0; n < 8; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[n][j] = o[n][j] = 0.f;
-        // y = (K S)^T in NT terms of S, o = (Q S)^T in one: this warp's part of the sum
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
             uint32_t fs[NT][4];
@@ -456,82 +526,105 @@ __global__ void __launch_bounds__(kAllThreads, 1) delta_chain_kernel(const Chain
             for (int np = 0; np < 4; ++np) {
                 uint32_t fb[4], fq[4];
                 ldsm(fb, kt + at<L::kRow>(np * 16 + br, k0 / 8 + 2 * ks + bc));
-                if (!CKPT) ldsm(fq, qt + at<L::kRow>(np * 16 + br, k0 / 8 + 2 * ks + bc));
+                if (MODE == kFwd) ldsm(fq, qt + at<L::kRow>(np * 16 + br, k0 / 8 + 2 * ks + bc));
 #pragma unroll
                 for (int t = NT - 1; t >= 0; --t) {
                     mma(y[2 * np], fs[t], fb[0], fb[1]);
                     mma(y[2 * np + 1], fs[t], fb[2], fb[3]);
                 }
-                if (!CKPT) {
+                if (MODE == kFwd) {
                     mma(o[2 * np], fs[0], fq[0], fq[1]);
                     mma(o[2 * np + 1], fs[0], fq[2], fq[3]);
                 }
             }
         }
         put_sums(y);
-        bar<32 * KS>(kBarSlice + slice);
-        // R = beta (V - e^G K S), the left operand of T
+        const float last = vec.last;
 #pragma unroll
-        for (int j = 0; j < OWN; j += 2) {
-            uint32_t fv[4];
-            ldsm_t(fv, vt + at<L::kValRow>((lane >> 4 ? own(j + 1) : own(j)) * 8 + (lane & 7), 2 * slice + bc));
+        for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int n = own(j + m);
-                float x[4];
-                get_sum(n, x);
-                const float2 e = *reinterpret_cast<const float2 *>(vec.e + 8 * n + q0);
-                const float2 be = *reinterpret_cast<const float2 *>(vec.beta + 8 * n + q0);
-                x[0] = be.x * fmaf(-e.x, x[0], low(fv[2 * m]));
-                x[1] = be.y * fmaf(-e.y, x[1], high(fv[2 * m]));
-                x[2] = be.x * fmaf(-e.x, x[2], low(fv[2 * m + 1]));
-                x[3] = be.y * fmaf(-e.y, x[3], high(fv[2 * m + 1]));
-                uint32_t t0[NT], t1[NT];
-                split<NT>(x[0], x[1], t0);
-                split<NT>(x[2], x[3], t1);
+            for (int j = 0; j < 4; ++j) S[n][j] *= last;
+        uint32_t fd[4][1][4];                            // kBack: dO^T as the left operand
+        if (BACK) {
+            // what does not wait for y: R += (scale e^G dO)^T Q
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    reinterpret_cast<uint2 *>(rows)[(t * 8 + n) * 32 + lane] = make_uint2(t0[t], t1[t]);
+            for (int kb = 0; kb < 4; ++kb) {
+                ldsm_t(fd[kb][0], vt + at<L::kValRow>(kb * 16 + br, 2 * slice + bc));
+                float z[2][4];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const float2 e = *reinterpret_cast<const float2 *>(vec.e + 16 * kb + 8 * m + q0);
+                    const float ex = p.scale * e.x, ey = p.scale * e.y;
+                    z[m][0] = ex * low(fd[kb][0][2 * m]); z[m][1] = ey * high(fd[kb][0][2 * m]);
+                    z[m][2] = ex * low(fd[kb][0][2 * m + 1]); z[m][3] = ey * high(fd[kb][0][2 * m + 1]);
+                }
+                add_outer(z[0], z[1], kb, qt);
             }
         }
-        bar<32 * KS>(kBarSlice + slice);
-        if (!CKPT) put_sums(o);
+        meet();
+        float x[OWN][4];
+        get_sums(y, x);
+        if (BACK) {
+            // dU = f K R + P^T dO
+#pragma unroll
+            for (int j = 0; j < OWN; ++j) {
+                const float2 f = *reinterpret_cast<const float2 *>(vec.f + 8 * own(j) + q0);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) x[j][m] *= (m & 1) ? f.y : f.x;
+            }
+            triangle(x, fd, pt, Int<1>{}, Int<2>{}, Int<1>{});
+        } else {
+            // R = beta (V - e^G K S)
+#pragma unroll
+            for (int j = 0; j < OWN; j += 2) {
+                uint32_t fv[4];
+                ldsm_t(fv, vt + at<L::kValRow>((lane >> 4 ? own(j + 1) : own(j)) * 8 + (lane & 7), 2 * slice + bc));
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const float2 e = *reinterpret_cast<const float2 *>(vec.e + 8 * own(j + m) + q0);
+                    const float2 be = *reinterpret_cast<const float2 *>(vec.beta + 8 * own(j + m) + q0);
+                    x[j + m][0] = be.x * fmaf(-e.x, x[j + m][0], low(fv[2 * m]));
+                    x[j + m][1] = be.y * fmaf(-e.y, x[j + m][1], high(fv[2 * m]));
+                    x[j + m][2] = be.x * fmaf(-e.x, x[j + m][2], low(fv[2 * m + 1]));
+                    x[j + m][3] = be.y * fmaf(-e.y, x[j + m][3], high(fv[2 * m + 1]));
+                }
+            }
+        }
+        // U = T R (kBack: X = T^T dU)
         uint32_t fr[4][NT][4];
+        offer_terms(x);
+        meet();
+        if (MODE == kFwd) put_sums(o);
+        take_terms(x, fr);
+        meet();
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb)
+        for (int j = 0; j < OWN; ++j)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const uint2 u0 = reinterpret_cast<const uint2 *>(rows)[(t * 8 + 2 * kb) * 32 + lane];
-                const uint2 u1 = reinterpret_cast<const uint2 *>(rows)[(t * 8 + 2 * kb + 1) * 32 + lane];
-                fr[kb][t][0] = u0.x; fr[kb][t][1] = u0.y; fr[kb][t][2] = u1.x; fr[kb][t][3] = u1.y;
+            for (int m = 0; m < 4; ++m) x[j][m] = 0.f;
+        triangle(x, fr, tt, Int<NT>{}, Int<NT>{}, Int<NT - 1>{});
+        if (MODE != kFwd) {
+#pragma unroll
+            for (int j = 0; j < OWN; ++j) {
+                const float2 be = *reinterpret_cast<const float2 *>(vec.beta + 8 * own(j) + q0);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int row = c * C + 8 * own(j) + q0 + (m & 1), cc = col + 8 * (m >> 1);
+                    const float bm = (m & 1) ? be.y : be.x;
+                    if (row < len && cc < p.dv) a.rows[(vrow + row) * p.dv + cc] = BACK ? x[j][m] : x[j][m] / bm;
+                    if (BACK) x[j][m] *= -bm;
+                }
             }
-        bar<32 * KS>(kBarSlice + slice);
-        // U^T = R^T T^T over the blocks at and below the diagonal
-        float u[OWN][4];
-#pragma unroll
-        for (int j = 0; j < OWN; ++j)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) u[j][m] = 0.f;
-        triangle(u, fr, tt, Int<NT>{}, Int<NT>{}, Int<NT - 1>{});
-#pragma unroll
-        for (int j = 0; j < OWN; ++j)
-            reinterpret_cast<float4 *>(rows)[own(j) * 32 + lane] = make_float4(u[j][0], u[j][1], u[j][2], u[j][3]);
-        bar<32 * KS>(kBarSlice + slice);
-        float z[8][4];
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const float4 x = reinterpret_cast<const float4 *>(rows)[n * 32 + lane];
-            z[n][0] = x.x; z[n][1] = x.y; z[n][2] = x.z; z[n][3] = x.w;
         }
-        if (!CKPT) {
+        float z[8][4];
+        share(x, z);
+        if (MODE == kFwd) {
             // O = scale e^G Q S + P U
             uint32_t fu[4][2][4];
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) split_a<2>(z[2 * kb], z[2 * kb + 1], fu[kb]);
-            float x[OWN][4];
+            get_sums(o, x);
 #pragma unroll
             for (int j = 0; j < OWN; ++j) {
-                get_sum(own(j), x[j]);
                 const float2 e = *reinterpret_cast<const float2 *>(vec.e + 8 * own(j) + q0);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) x[j][m] *= p.scale * ((m & 1) ? e.y : e.x);
@@ -549,45 +642,19 @@ __global__ void __launch_bounds__(kAllThreads, 1) delta_chain_kernel(const Chain
                     *reinterpret_cast<uint4 *>(out + (vrow + row) * p.dv + cc) =
                         *reinterpret_cast<const uint4 *>(st + L::oV + at<L::kValRow>(r, 2 * slice + bc));
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < OWN; ++j) {
-                const float2 be = *reinterpret_cast<const float2 *>(vec.beta + 8 * own(j) + q0);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int row = c * C + 8 * own(j) + q0 + (m & 1), cc = col + 8 * (m >> 1);
-                    if (row < len && cc < p.dv) a.w[(vrow + row) * p.dv + cc] = u[j][m] / ((m & 1) ? be.y : be.x);
-                }
-            }
         }
-        // S <- e^{G_C} S + (f U)^T K
-        const float last = vec.last;
-#pragma unroll
-        for (int n = 0; n < DK / 8; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) S[n][j] *= last;
+        // S += (f U)^T K  (kBack: R -= (e^G beta X)^T K)
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                const float2 f = *reinterpret_cast<const float2 *>(vec.f + 16 * kb + 8 * m + q0);
+                const float2 f = *reinterpret_cast<const float2 *>((BACK ? vec.e : vec.f) + 16 * kb + 8 * m + q0);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) z[2 * kb + m][j] *= (j & 1) ? f.y : f.x;
             }
-            uint32_t fs[NT][4];
-            split_a<NT>(z[2 * kb], z[2 * kb + 1], fs);
-#pragma unroll
-            for (int nd = 0; nd < DK / 16; ++nd) {
-                uint32_t fb[4];
-                ldsm_t(fb, kt + at<L::kRow>(kb * 16 + tr, k0 / 8 + 2 * nd + tc));
-#pragma unroll
-                for (int t = NT - 1; t >= 0; --t) {
-                    mma(S[2 * nd], fs[t], fb[0], fb[1]);
-                    mma(S[2 * nd + 1], fs[t], fb[2], fb[3]);
-                }
-            }
+            add_outer(z[2 * kb], z[2 * kb + 1], kb, kt);
         }
-        bar<kAllThreads>(kBarAll);
+        bar<kAll>(kBarAll);
     }
     if (a.state_out)
 #pragma unroll
@@ -608,24 +675,21 @@ cudaError_t prep(const DeltaProblem &p, char *chunks, bool held, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <int D, int NT, int SL, bool CKPT>
+template <int D, int NT, int SL, int KS, int MODE>
 cudaError_t chain(ChainArgs a, cudaStream_t s) {
+    using L = ChainSmem<D, NT, SL, KS>;
     a.groups = (a.p.dv + 16 * SL - 1) / (16 * SL);
-    constexpr int smem = ChainSmem<D, NT, SL>::total;
-    const cudaError_t e = set_dyn_smem((const void *)delta_chain_kernel<D, NT, SL, CKPT>, smem);
+    const cudaError_t e = set_dyn_smem((const void *)delta_chain_kernel<D, NT, SL, KS, MODE>, L::total);
     if (e != cudaSuccess) return e;
-    delta_chain_kernel<D, NT, SL, CKPT><<<(unsigned)(a.p.B * a.p.H * a.groups), kAllThreads, smem, s>>>(a);
+    delta_chain_kernel<D, NT, SL, KS, MODE><<<(unsigned)(a.p.B * a.p.H * a.groups), L::kAll, L::total, s>>>(a);
     return cudaGetLastError();
 }
 
-template <int D, int NT, bool CKPT>
-cudaError_t forward(const ChainArgs &a, cudaStream_t s) {
-    const cudaError_t e = prep<D, NT>(a.p, const_cast<char *>(a.chunks), CKPT, s);
-    if (e != cudaSuccess) return e;
-    // Eight chain warps to a CTA, one CTA to an SM: four warps to each 16 columns while that fits one wave of CTAs, two
-    // beyond (measured at 32 heads of 128 x 128: ... and 96 heads of 64 x 64: ...).
+template <int D, int NT, int MODE>
+cudaError_t chains(const ChainArgs &a, cudaStream_t s) {
     const long long heads = (long long)a.p.B * a.p.H;
-    return heads * ((a.p.dv + 31) / 32) <= 152 ? chain<D, NT, 2, CKPT>(a, s) : chain<D, NT, 4, CKPT>(a, s);
+    if (heads * ((a.p.dv + 31) / 32) <= 152) return chain<D, NT, 2, 4, MODE>(a, s);
+    return chain<D, NT, 4, 1, MODE>(a, s);
 }
 
 }  // namespace
@@ -641,8 +705,72 @@ size_t delta_tc_workspace(const DeltaProblem &p) {
 cudaError_t delta_tc_forward(const DeltaProblem &p, const float *state_in, void *out, float *state_out, char *ws,
                              cudaStream_t s) {
     const ChainArgs a{p, ws, (p.N + C - 1) / C, 0, state_in, state_out, out, nullptr, nullptr};
-    if (p.d <= 64) return state_out ? forward<64, 3, false>(a, s) : forward<64, 2, false>(a, s);
-    return state_out ? forward<128, 3, false>(a, s) : forward<128, 2, false>(a, s);
+    cudaError_t e = cudaSuccess;
+    auto both = [&](auto d, auto nt) {
+        constexpr int D = decltype(d)::value, NT = decltype(nt)::value;
+        e = prep<D, NT>(p, ws, false, s);
+        if (e == cudaSuccess) e = chains<D, NT, kFwd>(a, s);
+    };
+    if (p.d <= 64) state_out ? both(Int<64>{}, Int<3>{}) : both(Int<64>{}, Int<2>{});
+    else state_out ? both(Int<128>{}, Int<3>{}) : both(Int<128>{}, Int<2>{});
+    return e;
+}
+
+namespace {
+struct BackLayout {
+    size_t chunks, w, x, s0, ds, dq, dk, total;
+};
+BackLayout back_layout(const DeltaProblem &p) {
+    const size_t G = (size_t)p.B * p.H, rows = G * p.N, states = G * ((p.N + C - 1) / C) * p.d * p.dv;
+    BackLayout L{};
+    size_t o = 0;
+    auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes); return at; };
+    L.chunks = take(delta_tc_workspace(p));
+    L.w = take(rows * p.dv * 4);
+    L.x = take(rows * p.dv * 4);
+    L.s0 = take(states * 2);
+    L.ds = take(states * 2);
+    L.dq = p.H != p.Hk ? take(rows * p.d * 4) : 0;
+    L.dk = p.H != p.Hk ? take(rows * p.d * 4) : 0;
+    L.total = o;
+    return L;
+}
+}  // namespace
+
+size_t delta_tc_backward_workspace(const DeltaProblem &p) { return back_layout(p).total; }
+
+cudaError_t delta_tc_backward(const DeltaProblem &p, const float *state_in, const void *dO, const float *dstate_out,
+                              void *dQ, void *dK, void *dV, void *dg, void *dbeta, float *dstate_in, char *ws,
+                              cudaStream_t s) {
+    const BackLayout L = back_layout(p);
+    const int nc = (p.N + C - 1) / C;
+    char *chunks = ws + L.chunks;
+    const ChainArgs f{p, chunks, nc, 0, state_in, nullptr, nullptr, reinterpret_cast<float *>(ws + L.w),
+                      reinterpret_cast<__nv_bfloat16 *>(ws + L.s0)};
+    ChainArgs r{p, chunks, nc, 0, dstate_out, dstate_in, nullptr, reinterpret_cast<float *>(ws + L.x),
+                reinterpret_cast<__nv_bfloat16 *>(ws + L.ds)};
+    r.p.V = dO;
+    cudaError_t e = cudaSuccess;
+    int bytes = 0, vec_at = 0;
+    // three terms where the state's gradient is returned in fp32, as in the forward
+    auto run = [&](auto d, auto nt) {
+        constexpr int D = decltype(d)::value, NT = decltype(nt)::value;
+        bytes = Chunk<NT>::bytes;
+        vec_at = Chunk<NT>::oVec;
+        e = prep<D, NT>(p, chunks, true, s);
+        if (e == cudaSuccess) e = chains<D, NT, kCkpt>(f, s);
+        if (e == cudaSuccess) e = chains<D, NT, kBack>(r, s);
+    };
+    if (p.d <= 64) dstate_in ? run(Int<64>{}, Int<3>{}) : run(Int<64>{}, Int<2>{});
+    else dstate_in ? run(Int<128>{}, Int<3>{}) : run(Int<128>{}, Int<2>{});
+    if (e != cudaSuccess) return e;
+    const bool shared = p.H != p.Hk;
+    float *dq = shared ? reinterpret_cast<float *>(ws + L.dq) : nullptr;
+    float *dk = shared ? reinterpret_cast<float *>(ws + L.dk) : nullptr;
+    const DeltaTcGrads g{dO, chunks, f.rows, r.rows, f.states, r.states, dq, dk, dQ, dK, dV, dg, dbeta};
+    e = delta_tc_grads(p, g, bytes, vec_at, s);
+    if (e == cudaSuccess && shared) e = delta_sum_heads(p, dq, dk, dQ, dK, s);
+    return e;
 }
 
 }  // namespace gma
