@@ -44,7 +44,7 @@ cudaError_t delta_tc_forward(const DeltaProblem &p, const float *state_in, void 
 struct DeltaTcGrads {
     const void *dO;
     const char *chunks;
-    const float *w, *x;               // [G, N, dv]
+    const __nv_bfloat16 *w, *x;       // W and X in two bf16 terms, [2, G, N, dv]
     const __nv_bfloat16 *s0, *ds;     // [G, nc, dv, d]: S before, dL/dS after each chunk
     float *dq_heads, *dk_heads;       // [G, N, d] per value head; null when H == Hk
     void *dQ, *dK, *dV, *dg, *dbeta;

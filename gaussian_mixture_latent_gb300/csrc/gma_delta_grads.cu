@@ -9,11 +9,16 @@
 //     a_i = M's row sum i - its column sum i + scale e^{G_i} q_i.S dO_i - e^{G_i} k_i.S x_i,  b_j = e^{G_C - G_j} k_j.R u_j
 // (pairs with both rows on one side of t cancel in the sums of a as the same fp32 numbers).
 //
-// One CTA of twelve warps to a chunk, one warp of each role to a 16-row block: the first four make E1 and dQ, the next
-// four E2 and the query half of dK, the last four the transposed products and the key half.  An accumulator tile of E is
-// the next product's left operand as it stands; dv goes by in slabs of 64 columns.  u, x and E are taken in two bf16 terms
-// (2^-17), the two states in one: half a step of bf16 each, as the gradients' own rounding.
-// Bound by mma.sync issue (8 cycles each on a tensor unit), the rest is the latency of three warps a scheduler.
+// W and X come in two bf16 terms each; beta joins as a factor of rows and columns, and dbeta is the diagonal of X W^T.
+//
+// One CTA of twelve warps to a chunk, one warp of each role to a 16-row block.  First the four warps of role 0 make E1,
+// those of role 1 E2 (an accumulator tile times its decays, in two bf16 terms to shared memory), and role 2 the product
+// U R^T; then role 0 makes dQ, role 1 the query half of dK and role 2 the key half from the same E tiles, read transposed.
+// dv goes by in slabs of 64 columns; with one slab (ONE) the states' products wait until E is done, which leaves 80
+// registers a thread and two CTAs to an SM.
+// Precision: W, X and E in two bf16 terms (2^-17), the two states in one: half a bf16 step of their products, as the
+// gradients' own rounding.  Bound by the latency of few warps between barriers; the mma.sync issue alone is about
+// 3700 cycles a chunk at 64 x 64 (8 cycles each on a tensor unit).
 #include <cstdint>
 
 #include "gma_delta.h"
@@ -34,17 +39,18 @@ struct Args {
 
 template <int D>
 struct Smem {
-    static constexpr int kRow = 2 * D, kKey = C * kRow, kSlabRow = 128, kSlab = C * kSlabRow;
-    static constexpr int oQ = kKey, oDo = 2 * kKey, oU = oDo + kSlab, oX = oU + 2 * kSlab, oS = oX + 2 * kSlab, oR = oS + kKey;
-    static constexpr int oVec = oR + kKey, oRed = oVec + (int)sizeof(Vec);
+    static constexpr int kRow = 2 * D, kKey = C * kRow, kSlab = C * 128;
+    static constexpr int oQ = kKey, oDo = 2 * kKey, oW = oDo + kSlab, oX = oW + 2 * kSlab, oS = oX + 2 * kSlab, oR = oS + kKey;
+    static constexpr int oE = oR + kKey;                 // E1 and E2, two terms each, as packed triangles
+    static constexpr int oVec = oE + 4 * kTriBytes, oRed = oVec + (int)sizeof(Vec);
     static constexpr int kPitch = D + 8;                 // floats: the exchange of dK's halves, over the slab's tiles
-    static_assert(C * kPitch * 4 <= oVec - oDo, "the exchange fits");
+    static_assert(C * kPitch * 4 <= oE - oDo, "the exchange fits");
     // sums: rows [64] and columns [4][64] of both matrices, b [64], dbeta [64], inner [12]
     static constexpr int kRed = 64 + 64 + 256 + 256 + 64 + 64 + 16, total = oRed + kRed * 4;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const Args a) {
+template <int D, bool ONE>
+__global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_kernel(const Args a) {
     using L = Smem<D>;
     extern __shared__ __align__(128) char sm[];
     const uint32_t sb = smem_u32(sm);
@@ -74,6 +80,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const Args a) 
     }
     const __nv_bfloat16 *K = static_cast<const __nv_bfloat16 *>(p.Kx), *Q = static_cast<const __nv_bfloat16 *>(p.Qx);
     const __nv_bfloat16 *dO = static_cast<const __nv_bfloat16 *>(a.g.dO);
+    const size_t plane = (size_t)p.B * p.H * p.N * p.dv;
     Vec &vec = *reinterpret_cast<Vec *>(sm + L::oVec);
     float *row1 = reinterpret_cast<float *>(sm + L::oRed), *row2 = row1 + 64, *col1 = row2 + 64, *col2 = col1 + 256;
     float *keys = col2 + 256, *dbeta = keys + 64, *inner = dbeta + 64;
@@ -89,11 +96,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const Args a) 
     if (tid < (int)sizeof(Vec) / 16) copy16(sb + L::oVec + 16 * tid, chunk + 16 * tid, true);
     const __nv_bfloat16 *s0 = a.g.s0 + ((size_t)bh * a.nc + c) * p.dv * p.d, *ds = a.g.ds + ((size_t)bh * a.nc + c) * p.dv * p.d;
 
-    float e1[8][4], e2[8][4], acc[D / 8][4];             // E (role 0 and 1: one of them), the row block of dQ or dK
+    float e[8][4], acc[D / 8][4];                        // a row block of E (role 0, 1); of dQ or a half of dK
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) e1[i][j] = e2[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) e[i][j] = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
 #pragma unroll
@@ -101,15 +108,43 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const Args a) 
     const int ar = (lane & 7) + ((lane >> 3) & 1) * 8, ac = lane >> 4;      // A operand, and B transposed: row, piece
     const int br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;      // B operand of two n tiles
     const int r0 = lane >> 2, q0 = 2 * (lane & 3);
-    float in = 0.f, db = 0.f;
-    const int lr = tid >> 2;                             // row of the threads that read W and X
-    const float be = tid < 256 && lr < n ? delta_gate(p.beta, vrow + lr, p.gate_bf16) : 0.f;
+    const uint32_t ot = sb + L::oDo, wt = sb + L::oW, xt = sb + L::oX;
+    float in = 0.f;
+
+    // acc += the slab's part of dO S^T, X S^T or W R^T
+    auto state_product = [&] {
+        const uint32_t left = role == 0 ? ot : role == 1 ? xt : wt, st = sb + (role == 2 ? L::oR : L::oS);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t f[2][4];
+            ldsm(f[0], left + at<128>(rb * 16 + ar, 2 * ks + ac));
+            if (role) ldsm(f[1], left + L::kSlab + at<128>(rb * 16 + ar, 2 * ks + ac));
+#pragma unroll
+            for (int nd = 0; nd < D / 16; ++nd) {
+                uint32_t g[4];
+                ldsm_t(g, st + at<L::kRow>(ks * 16 + ar, 2 * nd + ac));
+                if (role) {
+                    mma(acc[2 * nd], f[1], g[0], g[1]);
+                    mma(acc[2 * nd + 1], f[1], g[2], g[3]);
+                }
+                mma(acc[2 * nd], f[0], g[0], g[1]);
+                mma(acc[2 * nd + 1], f[0], g[2], g[3]);
+            }
+        }
+    };
 
     for (int v0 = 0; v0 < p.dv; v0 += 64) {
         for (int i = tid; i < C * 8; i += kThreads) {
             const int r = i / 8, cc = i % 8;
             const bool ok = r < n && v0 + cc * 8 < p.dv;
-            copy16(sb + L::oDo + at<128>(r, cc), dO + (ok ? (vrow + r) * p.dv + v0 + cc * 8 : 0), ok);
+            const size_t off = ok ? (vrow + r) * p.dv + v0 + cc * 8 : 0;
+            const uint32_t to = at<128>(r, cc);
+            copy16(ot + to, dO + off, ok);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                copy16(wt + t * L::kSlab + to, a.g.w + t * plane + off, ok);
+                copy16(xt + t * L::kSlab + to, a.g.x + t * plane + off, ok);
+            }
         }
         for (int i = tid; i < 64 * (D / 8); i += kThreads) {
             const int r = i / (D / 8), cc = i % (D / 8);
@@ -119,99 +154,125 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const Args a) 
             copy16(sb + L::oR + at<L::kRow>(r, cc), ds + off, ok);
         }
         copy_commit();
-        if (tid < 256) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int cc = ((tid & 3) + 4 * m) * 4;
-                float4 w = make_float4(0.f, 0.f, 0.f, 0.f), x = w;
-                if (lr < n && v0 + cc < p.dv) {
-                    w = *reinterpret_cast<const float4 *>(a.g.w + (vrow + lr) * p.dv + v0 + cc);
-                    x = *reinterpret_cast<const float4 *>(a.g.x + (vrow + lr) * p.dv + v0 + cc);
-                }
-                db += w.x * x.x + w.y * x.y + w.z * x.z + w.w * x.w;
-                uint32_t u0[2], u1[2], x0[2], x1[2];
-                split<2>(be * w.x, be * w.y, u0);
-                split<2>(be * w.z, be * w.w, u1);
-                split<2>(be * x.x, be * x.y, x0);
-                split<2>(be * x.z, be * x.w, x1);
-                const uint32_t to = at<128>(lr, cc / 8) + (cc & 4) * 2;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    *reinterpret_cast<uint2 *>(sm + L::oU + t * L::kSlab + to) = make_uint2(u0[t], u1[t]);
-                    *reinterpret_cast<uint2 *>(sm + L::oX + t * L::kSlab + to) = make_uint2(x0[t], x1[t]);
-                }
-                if (lr < n_all && v0 + cc < p.dv)
-                    *reinterpret_cast<uint2 *>(dV + (vrow + lr) * p.dv + v0 + cc) = make_uint2(x0[0], x1[0]);
-            }
-        }
         copy_wait<0>();
         __syncthreads();
-        const uint32_t ut = sb + L::oU, xt = sb + L::oX, ot = sb + L::oDo;
-        const uint32_t st = sb + (role == 2 ? L::oR : L::oS);
+        if (role < 2) {
+            // E1: dO W^T, E2: X W^T
+            const uint32_t left = role == 0 ? ot : xt;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            // the left rows: dO, x or u; one term of dO, two of the others
-            uint32_t f[2][4];
-            const uint32_t lt = role == 0 ? ot : role == 1 ? xt : ut;
-            ldsm(f[0], lt + at<128>(rb * 16 + ar, 2 * ks + ac));
-            if (role) ldsm(f[1], lt + L::kSlab + at<128>(rb * 16 + ar, 2 * ks + ac));
+            for (int ks = 0; ks < 4; ++ks) {
+                uint32_t f[2][4];
+                ldsm(f[0], left + at<128>(rb * 16 + ar, 2 * ks + ac));
+                if (role) ldsm(f[1], left + L::kSlab + at<128>(rb * 16 + ar, 2 * ks + ac));
 #pragma unroll
-            for (int np = 0; np < 4; ++np) {
-                if (role == 2 ? np < rb : np > rb) continue;
-                uint32_t g0[4], g1[4];
-                const uint32_t o = at<128>(np * 16 + br, 2 * ks + bc);
-                if (role < 2) {
-                    ldsm(g0, ut + o);
-                    ldsm(g1, ut + L::kSlab + o);
-                    mma(e1[2 * np], f[0], g1[0], g1[1]);
-                    mma(e1[2 * np + 1], f[0], g1[2], g1[3]);
+                for (int np = 0; np < 4; ++np) {
+                    if (np > rb) continue;
+                    uint32_t g0[4], g1[4];
+                    const uint32_t o = at<128>(np * 16 + br, 2 * ks + bc);
+                    ldsm(g0, wt + o);
+                    ldsm(g1, wt + L::kSlab + o);
+                    mma(e[2 * np], f[0], g1[0], g1[1]);
+                    mma(e[2 * np + 1], f[0], g1[2], g1[3]);
                     if (role) {
-                        mma(e1[2 * np], f[1], g0[0], g0[1]);
-                        mma(e1[2 * np + 1], f[1], g0[2], g0[3]);
+                        mma(e[2 * np], f[1], g0[0], g0[1]);
+                        mma(e[2 * np + 1], f[1], g0[2], g0[3]);
                     }
-                    mma(e1[2 * np], f[0], g0[0], g0[1]);
-                    mma(e1[2 * np + 1], f[0], g0[2], g0[3]);
-                } else {
-                    uint32_t g2[4];
-                    ldsm(g0, ot + o);
-                    ldsm(g1, xt + o);
-                    ldsm(g2, xt + L::kSlab + o);
-                    mma(e1[2 * np], f[1], g0[0], g0[1]);
-                    mma(e1[2 * np + 1], f[1], g0[2], g0[3]);
-                    mma(e1[2 * np], f[0], g0[0], g0[1]);
-                    mma(e1[2 * np + 1], f[0], g0[2], g0[3]);
-                    mma(e2[2 * np], f[0], g2[0], g2[1]);
-                    mma(e2[2 * np + 1], f[0], g2[2], g2[3]);
-                    mma(e2[2 * np], f[1], g1[0], g1[1]);
-                    mma(e2[2 * np + 1], f[1], g1[2], g1[3]);
-                    mma(e2[2 * np], f[0], g1[0], g1[1]);
-                    mma(e2[2 * np + 1], f[0], g1[2], g1[3]);
+                    mma(e[2 * np], f[0], g0[0], g0[1]);
+                    mma(e[2 * np + 1], f[0], g0[2], g0[3]);
+                }
+            }
+        }
+        if (!ONE || role == 2) state_product();
+        if (role == 2) {
+            for (int i = tid - 256; i < 64 * D / 2; i += 128) {      // <S, R>: both tiles have the same layout
+                const uint32_t x = reinterpret_cast<const uint32_t *>(sm + L::oS)[i];
+                const uint32_t y = reinterpret_cast<const uint32_t *>(sm + L::oR)[i];
+                in = fmaf(low(x), low(y), fmaf(high(x), high(y), in));
+            }
+            for (int i = tid - 256; i < C * 8; i += 128) {           // dV = beta X
+                const int r = i / 8, cc = v0 + i % 8 * 8;
+                if (r >= n_all || cc >= p.dv) continue;
+                const float be = r < n ? delta_gate(p.beta, vrow + r, p.gate_bf16) : 0.f;
+                const uint4 x = *reinterpret_cast<const uint4 *>(sm + L::oX + at<128>(r, i % 8));
+                const uint4 y = *reinterpret_cast<const uint4 *>(sm + L::oX + L::kSlab + at<128>(r, i % 8));
+                auto both = [&](uint32_t h, uint32_t l) { return pack(be * (low(h) + low(l)), be * (high(h) + high(l))); };
+                *reinterpret_cast<uint4 *>(dV + (vrow + r) * p.dv + cc) =
+                    make_uint4(both(x.x, y.x), both(x.y, y.y), both(x.z, y.z), both(x.w, y.w));
+            }
+        }
+        if (!ONE) __syncthreads();
+    }
+    const int i0 = rb * 16 + r0, i1 = i0 + 8;
+    const uint32_t et = sb + L::oE;
+    float d0 = 0.f, d1 = 0.f;
+    if (role < 2) {
+        // E's decays, factors and masks; M = E o (Q or K) K^T: row sums and column sums; E's terms to shared memory
+        const float2 g0 = vec.G[i0], g1 = vec.G[i1];
+        const float m0 = role ? vec.beta[i0] : p.scale, m1 = role ? vec.beta[i1] : p.scale;
+        float *col = (role ? col2 : col1) + 64 * rb;
+        char *to = sm + L::oE + 2 * role * kTriBytes;
+        const uint32_t left = sb + (role == 0 ? L::oQ : 0);
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+            float qk[2][4] = {};
+            if (np <= rb) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    uint32_t f[4], g[4];
+                    ldsm(f, left + at<L::kRow>(rb * 16 + ar, 2 * ks + ac));
+                    ldsm(g, sb + at<L::kRow>(np * 16 + br, 2 * ks + bc));
+                    mma(qk[0], f, g[0], g[1]);
+                    mma(qk[1], f, g[2], g[3]);
                 }
             }
 #pragma unroll
-            for (int nd = 0; nd < D / 16; ++nd) {
-                uint32_t g0[4];
-                ldsm_t(g0, st + at<L::kRow>(ks * 16 + ar, 2 * nd + ac));
-                if (role) {
-                    mma(acc[2 * nd], f[1], g0[0], g0[1]);
-                    mma(acc[2 * nd + 1], f[1], g0[2], g0[3]);
+            for (int u = 0; u < 2; ++u) {
+                const int t = 2 * np + u, j = 8 * t + q0;
+                float x = 0.f, y = 0.f;
+                if (np <= rb) {
+                    const float4 gj = *reinterpret_cast<const float4 *>(vec.G + j);
+                    const float2 bj = *reinterpret_cast<const float2 *>(vec.beta + j);
+                    float dd[4] = {ex2((g0.x - gj.x) + (g0.y - gj.y)) * (m0 * bj.x), ex2((g0.x - gj.z) + (g0.y - gj.w)) * (m0 * bj.y),
+                                   ex2((g1.x - gj.x) + (g1.y - gj.y)) * (m1 * bj.x), ex2((g1.x - gj.z) + (g1.y - gj.w)) * (m1 * bj.y)};
+                    if (np == rb) {
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const int i = m < 2 ? i0 : i1, jj = j + (m & 1);
+                            if (role && jj == i) dbeta[i] = e[t][m];
+                            // a select and not a product with 0: what lies outside the triangle may be infinite
+                            e[t][m] = (role ? jj >= i : jj > i) ? 0.f : e[t][m] * dd[m];
+                        }
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) e[t][m] *= dd[m];
+                    }
+                    const float s0 = e[t][0] * qk[u][0], s1 = e[t][1] * qk[u][1], s2 = e[t][2] * qk[u][2], s3 = e[t][3] * qk[u][3];
+                    d0 += s0 + s1;
+                    d1 += s2 + s3;
+                    x = s0 + s2;
+                    y = s1 + s3;
+                    for (int o = 4; o < 32; o <<= 1) {
+                        x += __shfl_xor_sync(~0u, x, o);
+                        y += __shfl_xor_sync(~0u, y, o);
+                    }
+                    uint32_t w[2];
+                    const uint32_t blk = tri(rb, np) + 4 * (lane & 3);
+                    split<2>(e[t][0], e[t][1], w);
+                    *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0, u)) = w[0];
+                    *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0, u) + kTriBytes) = w[1];
+                    split<2>(e[t][2], e[t][3], w);
+                    *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0 + 8, u)) = w[0];
+                    *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0 + 8, u) + kTriBytes) = w[1];
                 }
-                mma(acc[2 * nd], f[0], g0[0], g0[1]);
-                mma(acc[2 * nd + 1], f[0], g0[2], g0[3]);
+                if (lane < 4) *reinterpret_cast<float2 *>(col + j) = make_float2(x, y);
             }
         }
-        for (int i = tid; i < 64 * D / 2; i += kThreads) {           // both tiles have the same layout
-            const uint32_t x = reinterpret_cast<const uint32_t *>(sm + L::oS)[i], y = reinterpret_cast<const uint32_t *>(sm + L::oR)[i];
-            in = fmaf(low(x), low(y), fmaf(high(x), high(y), in));
-        }
-        __syncthreads();
+        if (ONE) state_product();
     }
     // row factors of the state's product, and its dot with q (k): one number a row
-    const int i0 = rb * 16 + r0, i1 = i0 + 8;
-    const float m0 = role == 0 ? p.scale * vec.e[i0] : role == 1 ? vec.e[i0] : vec.f[i0];
-    const float m1 = role == 0 ? p.scale * vec.e[i1] : role == 1 ? vec.e[i1] : vec.f[i1];
+    const float m0 = role == 0 ? p.scale * vec.e[i0] : (role == 1 ? vec.e[i0] : vec.f[i0]) * vec.beta[i0];
+    const float m1 = role == 0 ? p.scale * vec.e[i1] : (role == 1 ? vec.e[i1] : vec.f[i1]) * vec.beta[i1];
     const char *own = sm + (role == 0 ? L::oQ : 0);
-    float d0 = 0.f, d1 = 0.f;
 #pragma unroll
     for (int t = 0; t < D / 8; ++t) {
         acc[t][0] *= m0; acc[t][1] *= m0; acc[t][2] *= m1; acc[t][3] *= m1;
@@ -219,72 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const Args a) 
         const uint32_t y = *reinterpret_cast<const uint32_t *>(own + at<L::kRow>(i1, t) + 2 * q0);
         d0 = fmaf(acc[t][0], low(x), fmaf(acc[t][1], high(x), d0));
         d1 = fmaf(acc[t][2], low(y), fmaf(acc[t][3], high(y), d1));
-    }
-    // E's decays and masks
-    const float2 g0 = vec.G[i0], g1 = vec.G[i1];
+        if (role == 1)                                   // dK takes its query half with the other sign
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-        if (role == 2 ? t / 2 < rb : t / 2 > rb) continue;
-        const int j = 8 * t + q0;
-        const float4 gj = *reinterpret_cast<const float4 *>(vec.G + j);
-        const float sg = role == 2 ? -1.f : 1.f;         // the transposed tiles: rows j, columns i
-        float dd[4] = {ex2(sg * ((g0.x - gj.x) + (g0.y - gj.y))), ex2(sg * ((g0.x - gj.z) + (g0.y - gj.w))),
-                       ex2(sg * ((g1.x - gj.x) + (g1.y - gj.y))), ex2(sg * ((g1.x - gj.z) + (g1.y - gj.w)))};
-        if (t / 2 == rb) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int i = m < 2 ? i0 : i1, jj = j + (m & 1);
-                if (role == 2 ? jj < i : jj > i) dd[m] = 0.f;
-                if (role == 1 && jj == i) dd[m] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int i = m < 2 ? i0 : i1, jj = j + (m & 1);
-            // a select and not a product with 0: what lies outside the triangle may be infinite
-            const float w = dd[m] == 0.f ? 0.f : e1[t][m] * dd[m];
-            e1[t][m] = role == 1 ? w : p.scale * w;
-            if (role == 2) e2[t][m] = dd[m] == 0.f || jj == i ? 0.f : e2[t][m] * dd[m];
-        }
-    }
-    if (role < 2) {
-        // M = E o (Q or K) K^T: row sums and column sums
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) e2[t][j] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t f[4];
-            ldsm(f, sb + (role == 0 ? L::oQ : 0) + at<L::kRow>(rb * 16 + ar, 2 * ks + ac));
-#pragma unroll
-            for (int np = 0; np < 4; ++np) {
-                if (np > rb) continue;
-                uint32_t g[4];
-                ldsm(g, sb + at<L::kRow>(np * 16 + br, 2 * ks + bc));
-                mma(e2[2 * np], f, g[0], g[1]);
-                mma(e2[2 * np + 1], f, g[2], g[3]);
-            }
-        }
-        float *col = (role ? col2 : col1) + 64 * rb;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            float x = 0.f, y = 0.f;
-            if (t / 2 <= rb) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) e2[t][m] *= e1[t][m];
-                // role 1's sums are subtracted: M's row sums join the row's dot with the same sign
-                d0 += e2[t][0] + e2[t][1];
-                d1 += e2[t][2] + e2[t][3];
-                x = e2[t][0] + e2[t][2];
-                y = e2[t][1] + e2[t][3];
-                for (int o = 4; o < 32; o <<= 1) {
-                    x += __shfl_xor_sync(~0u, x, o);
-                    y += __shfl_xor_sync(~0u, y, o);
-                }
-            }
-            if (lane < 4) *reinterpret_cast<float2 *>(col + 8 * t + q0) = make_float2(x, y);
-        }
+            for (int m = 0; m < 4; ++m) acc[t][m] = -acc[t][m];
     }
     d0 += __shfl_xor_sync(~0u, d0, 1); d0 += __shfl_xor_sync(~0u, d0, 2);
     d1 += __shfl_xor_sync(~0u, d1, 1); d1 += __shfl_xor_sync(~0u, d1, 2);
@@ -293,43 +291,44 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const Args a) 
         line[i0] = d0;
         line[i1] = d1;
     }
-    for (int o = 16; o; o >>= 1) in += __shfl_xor_sync(~0u, in, o);
-    if (lane == 0) inner[warp] = in;
-    db += __shfl_xor_sync(~0u, db, 1); db += __shfl_xor_sync(~0u, db, 2);
-    if (tid < 256 && (tid & 3) == 0) dbeta[lr] = db;
+    if (role == 2) {
+        for (int o = 16; o; o >>= 1) in += __shfl_xor_sync(~0u, in, o);
+        if (lane == 0) inner[rb] = in;
+    }
+    __syncthreads();
 
-    // acc += E K (role 0 and 1), E1^T Q - E2^T K (role 2)
+    // acc += E1 K (role 0), - E2 K (role 1), E1^T Q - E2^T K (role 2)
+    auto add_e = [&](int which, bool minus, uint32_t right) {
 #pragma unroll
-    for (int kb = 0; kb < 4; ++kb) {
-        if (role == 2 ? kb < rb : kb > rb) continue;
-        uint32_t f1[2][4], f2[2][4];
-        split_a<2>(e1[2 * kb], e1[2 * kb + 1], f1);
-        if (role == 2) {
+        for (int kb = 0; kb < 4; ++kb) {
+            if (role == 2 ? kb < rb : kb > rb) continue;
+            uint32_t f[2][4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                e2[2 * kb][m] = -e2[2 * kb][m];
-                e2[2 * kb + 1][m] = -e2[2 * kb + 1][m];
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t blk = et + (2 * which + t) * kTriBytes;
+                if (role == 2) ldsm_t(f[t], blk + tri(kb, rb) + at<32>(br, bc));
+                else ldsm(f[t], blk + tri(rb, kb) + at<32>(ar, ac));
+                if (minus)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) f[t][m] ^= 0x80008000u;
             }
-            split_a<2>(e2[2 * kb], e2[2 * kb + 1], f2);
-        }
 #pragma unroll
-        for (int nd = 0; nd < D / 16; ++nd) {
-            uint32_t g[4];
-            ldsm_t(g, sb + (role == 2 ? L::oQ : 0) + at<L::kRow>(kb * 16 + ar, 2 * nd + ac));
-#pragma unroll
-            for (int t = 1; t >= 0; --t) {
-                mma(acc[2 * nd], f1[t], g[0], g[1]);
-                mma(acc[2 * nd + 1], f1[t], g[2], g[3]);
-            }
-            if (role == 2) {
-                ldsm_t(g, sb + at<L::kRow>(kb * 16 + ar, 2 * nd + ac));
+            for (int nd = 0; nd < D / 16; ++nd) {
+                uint32_t g[4];
+                ldsm_t(g, right + at<L::kRow>(kb * 16 + ar, 2 * nd + ac));
 #pragma unroll
                 for (int t = 1; t >= 0; --t) {
-                    mma(acc[2 * nd], f2[t], g[0], g[1]);
-                    mma(acc[2 * nd + 1], f2[t], g[2], g[3]);
+                    mma(acc[2 * nd], f[t], g[0], g[1]);
+                    mma(acc[2 * nd + 1], f[t], g[2], g[3]);
                 }
             }
         }
+    };
+    if (role == 0) {
+        add_e(0, false, sb);
+    } else {
+        if (role == 2) add_e(0, false, sb + L::oQ);
+        add_e(1, true, sb);
     }
     float *half = reinterpret_cast<float *>(sm + L::oDo);            // the slabs are done with
     if (role == 0) {
@@ -351,14 +350,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const Args a) 
         for (int t = 0; t < D / 8; ++t) {
             const float2 x = *reinterpret_cast<const float2 *>(half + i0 * L::kPitch + 8 * t + q0);
             const float2 y = *reinterpret_cast<const float2 *>(half + i1 * L::kPitch + 8 * t + q0);
-            store2(dK, a.g.dk_heads, i0, 8 * t + q0, x.x - acc[t][0], x.y - acc[t][1]);
-            store2(dK, a.g.dk_heads, i1, 8 * t + q0, y.x - acc[t][2], y.y - acc[t][3]);
+            store2(dK, a.g.dk_heads, i0, 8 * t + q0, x.x + acc[t][0], x.y + acc[t][1]);
+            store2(dK, a.g.dk_heads, i1, 8 * t + q0, y.x + acc[t][2], y.y + acc[t][3]);
         }
     }
     if (warp == 0) {
         // a: rows and columns of both matrices; running sums from the end of a, from the start of b (two rows to a lane)
         float av[2], bv[2], tot = 0.f;
-        for (int w = 0; w < 12; ++w) tot += inner[w];
+        for (int w = 0; w < 4; ++w) tot += inner[w];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const int i = 2 * lane + m;
@@ -388,11 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const Args a) 
     }
 }
 
-template <int D>
+template <int D, bool ONE>
 cudaError_t launch(const Args &a, cudaStream_t s) {
-    const cudaError_t e = set_dyn_smem((const void *)delta_grads_kernel<D>, Smem<D>::total);
+    const cudaError_t e = set_dyn_smem((const void *)delta_grads_kernel<D, ONE>, Smem<D>::total);
     if (e != cudaSuccess) return e;
-    delta_grads_kernel<D><<<(unsigned)((size_t)a.p.B * a.p.H * a.nc), kThreads, Smem<D>::total, s>>>(a);
+    delta_grads_kernel<D, ONE><<<(unsigned)((size_t)a.p.B * a.p.H * a.nc), kThreads, Smem<D>::total, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -400,7 +399,8 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
 
 cudaError_t delta_tc_grads(const DeltaProblem &p, const DeltaTcGrads &g, int chunk_bytes, int vec_at, cudaStream_t s) {
     const Args a{p, g, (p.N + C - 1) / C, chunk_bytes, vec_at};
-    return p.d <= 64 ? launch<64>(a, s) : launch<128>(a, s);
+    if (p.dv <= 64) return p.d <= 64 ? launch<64, true>(a, s) : launch<128, true>(a, s);
+    return p.d <= 64 ? launch<64, false>(a, s) : launch<128, false>(a, s);
 }
 
 }  // namespace gma

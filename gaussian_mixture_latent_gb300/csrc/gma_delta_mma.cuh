@@ -152,6 +152,7 @@ struct Int { static constexpr int value = V; };
 struct Vec {                           // one chunk's row factors
     float2 G[kTcRows];                       // running sum of the log2 decays, hi + lo
     float e[kTcRows], f[kTcRows], beta[kTcRows];         // e^G, e^{G_C - G}
+    float ibeta[kTcRows];              // 1 / beta, for the backward
     float last, pad[3];                // e^{G_C}
 };
 // One chunk in the workspace: T's NT terms and P's two, as packed triangles, then the factors.

@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(const PrepA
             vec.e[2 * lane + j] = ex2(G.x);
             vec.f[2 * lane + j] = nan ? __int_as_float(0x7fffffff) : ex2(fixed_pair(end - q).x);
             vec.beta[2 * lane + j] = bn[j];
+            vec.ibeta[2 * lane + j] = a.held ? 1.f / bn[j] : 0.f;
         }
         if (lane == 31) vec.last = vec.e[C - 1];
     }
@@ -282,7 +283,7 @@ struct ChainArgs {
     const float *state_in;             // kBack: dL/dS after the last row
     float *state_out;                  // kBack: dL/dS before the first
     void *out;                         // kFwd
-    float *rows;                       // kCkpt: W, kBack: X, [G, N, dv]
+    __nv_bfloat16 *rows;               // kCkpt: W, kBack: X, as two bf16 terms [2, G, N, dv]
     __nv_bfloat16 *states;             // kCkpt: S before, kBack: R after each chunk, [G, nc, dv, d]
 };
 
@@ -479,6 +480,22 @@ __global__ void __launch_bounds__(32 * SL * KS + kLoadThreads, 1) delta_chain_ke
             }
         }
     };
+    // the warp's tiles [16 columns, 8 rows] as bf16 rows through the chunk's own V columns to memory
+    auto to_memory = [&](__nv_bfloat16 *to, int c, char *st, auto tile) {
+#pragma unroll
+        for (int j = 0; j < OWN; j += 2) {
+            const int r = (lane >> 4 ? own(j + 1) : own(j)) * 8 + (lane & 7);
+            char *mine = st + L::oV + at<L::kValRow>(r, 2 * slice + bc);
+            uint32_t x[2], y[2];
+            tile(j, x);
+            tile(j + 1, y);
+            stsm_t(smem_u32(mine), x[0], x[1], y[0], y[1]);
+            __syncwarp();
+            const int cc = c0 + 16 * slice + bc * 8, row = c * C + r;
+            if (row < len && cc < p.dv)
+                *reinterpret_cast<uint4 *>(to + (vrow + row) * p.dv + cc) = *reinterpret_cast<const uint4 *>(mine);
+        }
+    };
     // S += Z^T B for the warp's columns, Z in NT terms, B the rows of a tile
     auto add_outer = [&](const float (&z0)[4], const float (&z1)[4], int kb, uint32_t tile) {
         uint32_t fs[NT][4];
@@ -603,16 +620,23 @@ __global__ void __launch_bounds__(32 * SL * KS + kLoadThreads, 1) delta_chain_ke
             for (int m = 0; m < 4; ++m) x[j][m] = 0.f;
         triangle(x, fr, tt, Int<NT>{}, Int<NT>{}, Int<NT - 1>{});
         if (MODE != kFwd) {
+            // W (X) in two bf16 terms through the chunk's own V columns to memory
+            uint32_t t0[OWN][2], t1[OWN][2];
 #pragma unroll
             for (int j = 0; j < OWN; ++j) {
+                const float2 ib = *reinterpret_cast<const float2 *>(vec.ibeta + 8 * own(j) + q0);
                 const float2 be = *reinterpret_cast<const float2 *>(vec.beta + 8 * own(j) + q0);
+                split<2>(BACK ? x[j][0] : x[j][0] * ib.x, BACK ? x[j][1] : x[j][1] * ib.y, t0[j]);
+                split<2>(BACK ? x[j][2] : x[j][2] * ib.x, BACK ? x[j][3] : x[j][3] * ib.y, t1[j]);
+                if (BACK)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int row = c * C + 8 * own(j) + q0 + (m & 1), cc = col + 8 * (m >> 1);
-                    const float bm = (m & 1) ? be.y : be.x;
-                    if (row < len && cc < p.dv) a.rows[(vrow + row) * p.dv + cc] = BACK ? x[j][m] : x[j][m] / bm;
-                    if (BACK) x[j][m] *= -bm;
-                }
+                    for (int m = 0; m < 4; ++m) x[j][m] *= (m & 1) ? -be.y : -be.x;
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                __syncwarp();
+                to_memory(a.rows + t * (size_t)p.B * p.H * p.N * p.dv, c, st,
+                          [&](int j, uint32_t (&r)[2]) { r[0] = t0[j][t]; r[1] = t1[j][t]; });
             }
         }
         float z[8][4];
@@ -630,18 +654,7 @@ __global__ void __launch_bounds__(32 * SL * KS + kLoadThreads, 1) delta_chain_ke
                 for (int m = 0; m < 4; ++m) x[j][m] *= p.scale * ((m & 1) ? e.y : e.x);
             }
             triangle(x, fu, pt, Int<2>{}, Int<2>{}, Int<1>{});
-            // through the chunk's own V columns to memory
-#pragma unroll
-            for (int j = 0; j < OWN; j += 2) {
-                const int r = (lane >> 4 ? own(j + 1) : own(j)) * 8 + (lane & 7);
-                stsm_t(vt + at<L::kValRow>(r, 2 * slice + bc), pack(x[j][0], x[j][1]), pack(x[j][2], x[j][3]),
-                       pack(x[j + 1][0], x[j + 1][1]), pack(x[j + 1][2], x[j + 1][3]));
-                __syncwarp();
-                const int cc = c0 + 16 * slice + bc * 8, row = c * C + r;
-                if (row < len && cc < p.dv)
-                    *reinterpret_cast<uint4 *>(out + (vrow + row) * p.dv + cc) =
-                        *reinterpret_cast<const uint4 *>(st + L::oV + at<L::kValRow>(r, 2 * slice + bc));
-            }
+            to_memory(out, c, st, [&](int j, uint32_t (&r)[2]) { r[0] = pack(x[j][0], x[j][1]); r[1] = pack(x[j][2], x[j][3]); });
         }
         // S += (f U)^T K  (kBack: R -= (e^G beta X)^T K)
 #pragma unroll
@@ -745,9 +758,9 @@ cudaError_t delta_tc_backward(const DeltaProblem &p, const float *state_in, cons
     const BackLayout L = back_layout(p);
     const int nc = (p.N + C - 1) / C;
     char *chunks = ws + L.chunks;
-    const ChainArgs f{p, chunks, nc, 0, state_in, nullptr, nullptr, reinterpret_cast<float *>(ws + L.w),
+    const ChainArgs f{p, chunks, nc, 0, state_in, nullptr, nullptr, reinterpret_cast<__nv_bfloat16 *>(ws + L.w),
                       reinterpret_cast<__nv_bfloat16 *>(ws + L.s0)};
-    ChainArgs r{p, chunks, nc, 0, dstate_out, dstate_in, nullptr, reinterpret_cast<float *>(ws + L.x),
+    ChainArgs r{p, chunks, nc, 0, dstate_out, dstate_in, nullptr, reinterpret_cast<__nv_bfloat16 *>(ws + L.x),
                 reinterpret_cast<__nv_bfloat16 *>(ws + L.ds)};
     r.p.V = dO;
     cudaError_t e = cudaSuccess;
