@@ -42,12 +42,12 @@ struct PrepArgs {
 template <int D>
 struct PrepSmem {
     static constexpr int kRow = 2 * D, kKey = C * kRow;
-    static constexpr int oQ = kKey, oA = 2 * kKey, oI = oA + C * kFp * 4, oX = oI + C * kFp * 4;
-    static constexpr int oVec = oX + 4 * 32 * 12 * 4, total = oVec + (int)sizeof(Vec);
+    static constexpr int oQ = kKey, oA = 2 * kKey, oI = oA + C * kFp * 4;
+    static constexpr int oVec = oI + C * kFp * 4, total = oVec + (int)sizeof(Vec);
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(const PrepArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kernel(const PrepArgs a) {
     using L = PrepSmem<D>;
     using W = Chunk<NT>;
     constexpr int kRow = L::kRow;
@@ -73,7 +73,6 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(const PrepA
     }
     copy_commit();
     float *A = reinterpret_cast<float *>(sm + L::oA), *I = reinterpret_cast<float *>(sm + L::oI);
-    float *X = reinterpret_cast<float *>(sm + L::oX) + pw * 32 * 12;
     Vec &vec = *reinterpret_cast<Vec *>(sm + L::oVec);
     const int r0 = lane >> 2, q0 = 2 * (lane & 3);
     if (pt < 32) {
@@ -136,22 +135,27 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(const PrepA
     }
     const int i0 = rb * 16 + r0, i1 = i0 + 8;
     const float2 g0 = vec.G[i0], g1 = vec.G[i1];
+    const float2 gr = vec.G[rb * 16];
     const float m0 = inv ? vec.beta[i0] : p.scale, m1 = inv ? vec.beta[i1] : p.scale;
+    const float a0 = m0 * ex2((g0.x - gr.x) + (g0.y - gr.y)), a1 = m1 * ex2((g1.x - gr.x) + (g1.y - gr.y));
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
         if (n / 2 > rb) continue;
         const int j = 8 * n + q0;
         const float4 gj = *reinterpret_cast<const float4 *>(vec.G + j);      // hi, lo of rows j and j + 1
-        x[n][0] *= ex2((g0.x - gj.x) + (g0.y - gj.y)) * m0;
-        x[n][1] *= ex2((g0.x - gj.z) + (g0.y - gj.w)) * m0;
-        x[n][2] *= ex2((g1.x - gj.x) + (g1.y - gj.y)) * m1;
-        x[n][3] *= ex2((g1.x - gj.z) + (g1.y - gj.w)) * m1;
-        if (n / 2 == rb) {                       // the diagonal block: below (and, for P, on) the diagonal
+        if (n / 2 < rb) {
+            // the decay by way of the row block's first row: both factors' exponents are <= 0
+            const float bx = ex2((gr.x - gj.x) + (gr.y - gj.y)), by = ex2((gr.x - gj.z) + (gr.y - gj.w));
+            x[n][0] *= a0 * bx;
+            x[n][1] *= a0 * by;
+            x[n][2] *= a1 * bx;
+            x[n][3] *= a1 * by;
+        } else {                                         // the diagonal block: below (and, for P, on) the diagonal
             const int on = inv ? 0 : 1;
-            if (j >= i0 + on) x[n][0] = 0.f;
-            if (j + 1 >= i0 + on) x[n][1] = 0.f;
-            if (j >= i1 + on) x[n][2] = 0.f;
-            if (j + 1 >= i1 + on) x[n][3] = 0.f;
+            x[n][0] = j < i0 + on ? x[n][0] * (ex2((g0.x - gj.x) + (g0.y - gj.y)) * m0) : 0.f;
+            x[n][1] = j + 1 < i0 + on ? x[n][1] * (ex2((g0.x - gj.z) + (g0.y - gj.w)) * m0) : 0.f;
+            x[n][2] = j < i1 + on ? x[n][2] * (ex2((g1.x - gj.x) + (g1.y - gj.y)) * m1) : 0.f;
+            x[n][3] = j + 1 < i1 + on ? x[n][3] * (ex2((g1.x - gj.z) + (g1.y - gj.w)) * m1) : 0.f;
         }
         if (inv) {
             *reinterpret_cast<float2 *>(A + i0 * kFp + j) = make_float2(x[n][0], x[n][1]);
@@ -199,11 +203,12 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(const PrepA
             frag_a32<NT>(A + (lo + 16) * kFp + lo, kFp, lane, fa);
             frag_b32<NT>(I + lo * kFp + col, kFp, lane, fb);
             mma32<NT>(y, fa, fb);
-            *reinterpret_cast<float2 *>(X + r0 * 12 + q0) = make_float2(y[0], y[1]);
-            *reinterpret_cast<float2 *>(X + (r0 + 8) * 12 + q0) = make_float2(y[2], y[3]);
+            float *X = I + lo * kFp + col + 16;          // in between: above the diagonal, where nothing is kept
+            *reinterpret_cast<float2 *>(X + r0 * kFp + q0) = make_float2(y[0], y[1]);
+            *reinterpret_cast<float2 *>(X + (r0 + 8) * kFp + q0) = make_float2(y[2], y[3]);
             __syncwarp();
             frag_a32<NT>(I + (lo + 16) * kFp + lo + 16, kFp, lane, fa);
-            frag_b32<NT>(X, 12, lane, fb);
+            frag_b32<NT>(X, kFp, lane, fb);
             mma32<NT>(z, fa, fb);
             float *to = I + (lo + 16 + r0) * kFp + col + q0;
             *reinterpret_cast<float2 *>(to) = make_float2(-z[0], -z[1]);
@@ -222,15 +227,15 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(const PrepA
             frag_b32<NT>(I + 16 * k * kFp + col, kFp, lane, fb);
             mma32<NT>(y, fa, fb);
         }
-        float *to = X + (16 * m + r0) * 12 + q0;
+        float *X = I + 32 + col, *to = X + (16 * m + r0) * kFp + q0;
         *reinterpret_cast<float2 *>(to) = make_float2(y[0], y[1]);
-        *reinterpret_cast<float2 *>(to + 8 * 12) = make_float2(y[2], y[3]);
+        *reinterpret_cast<float2 *>(to + 8 * kFp) = make_float2(y[2], y[3]);
         bar<64>(kBarPair + pw);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (k > m) continue;
             frag_a32<NT>(I + (32 + 16 * m) * kFp + 32 + 16 * k, kFp, lane, fa);
-            frag_b32<NT>(X + 16 * k * 12, 12, lane, fb);
+            frag_b32<NT>(X + 16 * k * kFp, kFp, lane, fb);
             mma32<NT>(z, fa, fb);
         }
         to = I + (32 + 16 * m + r0) * kFp + col + q0;
