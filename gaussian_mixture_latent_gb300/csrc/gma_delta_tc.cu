@@ -257,14 +257,18 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kern
 }
 
 // -------------------------------------------------------------------------------------------------- delta_chain
-// The state never leaves registers.  KS warps share 16 columns of dv; each holds its part of S^T, [16, D / KS], as fp32
-// accumulator tiles.  Written transposed, every product of a chunk has such a tile on its left:
-//   (K S)^T = S^T K^T,  U^T = R^T T^T,  O^T = S^T Q^T + U^T P^T,  S^T += (f U)^T K,
+// The chunks of a head one after another; the state never leaves registers.  Four chain warps to a CTA: KS warps share 16
+// columns of dv (a slice), each holding its part of S^T, [16, D / KS], as fp32 accumulator tiles.  Written transposed,
+// every product of a chunk has such a tile on its left:
+//   (K S)^T = S^T K^T,  U^T = R^T T^T,  S^T += (f U)^T K,  and beside the chain O^T = S^T Q^T + U^T P^T,
 // and an accumulator tile is the next product's A operand as it stands.  The right sides (K, Q, T, P) are read from
-// shared memory with ldmatrix; four loader warps copy chunk c + kStages - 1 while chunk c is worked on.
+// shared memory with ldmatrix.
 // KS > 1: the warps split the first product's sum (their parts of d), then the 64 rows (eight-row tiles r, 7 - r, ..: the
 // same work under the triangles), then the columns of S^T; in between they exchange partial sums, R and U through shared
 // memory, lane by lane.
+// A helper warp to each slice takes what the next chunk does not wait for.  kFwd: O, from the state (one bf16 term) and U
+// that the chain leaves in shared memory.  kCkpt and kBack: the stores; kBack also the products of dO with P and Q, which
+// the chain adds.  Four loader warps copy chunk c + kStages - 1 while chunk c is worked on.
 //
 // kCkpt (for the backward): no O; writes S before each chunk (bf16, [dv, d]) and W = U / beta, with |beta| held to at
 // least 2^-64 (a beta of 0 then adds 2^-64 W to the state, nothing in fp32).
@@ -277,9 +281,10 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kern
 // but its accumulators are in TMEM: three dependent products a chunk would each pay a round trip (load, split, store,
 // fence, issue) of about a chunk's time here.
 enum Mode { kFwd, kCkpt, kBack };
-constexpr int kLoadThreads = 128;
-constexpr int kLoadRegs = 40;
-enum { kBarAll = 1, kBarSlice = 2 };   // named barriers; the slices use 2..5
+constexpr int kGroup = 128;            // threads of the chain, of the helpers (SL of the four warps work), of the loaders
+// Registers: launched with 168 a thread, 3 x 128 x 168 = 64512 = 128 x (240 + 192 + 72).
+constexpr int kChainRegs = 240, kHelpRegs = 192, kLoadRegs = 72;
+enum { kBarAll = 1, kBarSlice = 2, kBarU = 6, kBarZ = 10 };          // named barriers; one each of the last three to a slice
 
 struct ChainArgs {
     DeltaProblem p;                    // kBack: V is dO
@@ -292,29 +297,92 @@ struct ChainArgs {
     __nv_bfloat16 *states;             // kCkpt: S before, kBack: R after each chunk, [G, nc, dv, d]
 };
 
-template <int D, int NT, int SL, int KS>
+template <int D, int NT, int SL, int MODE>
 struct ChainSmem {
-    static constexpr int kThreads = 32 * SL * KS, kAll = kThreads + kLoadThreads;
-    // Registers.  Eight chain warps: launched with 168 a thread, 384 x 168 = 64512 = 256 x 232 + 128 x 40.  Fewer need no split.
-    static constexpr bool kSplit = kThreads == 256;
-    static constexpr int kChainRegs = 232;
+    static constexpr int KS = 4 / SL;
     static constexpr int kRow = 2 * D, kKey = C * kRow, kValRow = 32 * SL, kVal = C * kValRow;
     static constexpr int oQ = kKey, oV = 2 * kKey, oW = oV + kVal, kStage = oW + Chunk<NT>::bytes;
-    static constexpr int kSum = KS > 1 ? KS * 4096 : 0, kRows = KS > 1 ? 2048 * (NT > 2 ? NT : 2) : 0;    // of one slice
-    static constexpr int kShared = SL * (kSum + kRows);
-    static constexpr int kStages = 3 * kStage + kShared <= 227 * 1024 ? 3 : 2;
-    static constexpr int oSum = kStages * kStage, oRows = oSum + SL * kSum, total = oRows + SL * kRows;
+    // of one slice: partial sums; R's terms, then U (float4 [8 tiles][32 lanes]); the state in bf16; kBack: P^T dO and Q^T dO
+    static constexpr int kSum = KS > 1 ? KS * 4096 : 0, kRows = KS > 1 && NT > 2 ? 6144 : 4096, kState = 32 * D;
+    static constexpr int kZ = MODE == kBack ? 4096 + 64 * D : 0;
+    static constexpr int oRows = kSum, oState = oRows + kRows, oZ = oState + kState, kSlice = oZ + kZ;
+    static constexpr int kStages = 3 * kStage + SL * kSlice <= 227 * 1024 ? 3 : 2;
+    static constexpr int oSlice = kStages * kStage, total = oSlice + SL * kSlice;
     static_assert(total <= 227 * 1024, "shared memory");
 };
 
-template <int D, int NT, int SL, int KS, int MODE>
-__global__ void __launch_bounds__(32 * SL * KS + kLoadThreads, 1) delta_chain_kernel(const ChainArgs a) {
-    using L = ChainSmem<D, NT, SL, KS>;
+// x += F^T M^T (BACK: F^T M) for N eight-row tiles tile(j), M a packed triangle at t0: FT terms of F, TT of M, and of
+// their products those whose terms' indexes sum to MOST at most.
+template <bool BACK, int TT, int MOST, int N, int FT, class Tile>
+__device__ __forceinline__ void triangle(float (&x)[N][4], const uint32_t (&f)[4][FT][4], uint32_t t0, int lane, Tile tile) {
+    const int bc = (lane >> 3) & 1;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int n = tile(j), nb = n >> 1;
+#pragma unroll
+        for (int kb = 0; kb < 4; kb += 2) {
+            // blocks kb and kb + 1 along the sum; one outside the triangle is read as its neighbour and not used
+            const bool one = BACK ? kb >= nb : kb <= nb, two = BACK ? kb + 1 >= nb : kb + 1 <= nb;
+            if (!one && !two) continue;
+            const int k = kb + (lane >> 4);
+            const uint32_t blk = t0 + (BACK ? tri(max(k, nb), nb) + at<32>(lane & 15, n & 1)
+                                            : tri(nb, min(k, nb)) + at<32>((n & 1) * 8 + (lane & 7), bc));
+#pragma unroll
+            for (int t = TT - 1; t >= 0; --t) {
+                uint32_t fb[4];
+                if (BACK) ldsm_t(fb, blk + t * kTriBytes);
+                else ldsm(fb, blk + t * kTriBytes);
+#pragma unroll
+                for (int s = FT - 1; s >= 0; --s) {
+                    if (s + t > MOST) continue;
+                    if (one) mma(x[j], f[kb][s], fb[0], fb[1]);
+                    if (two) mma(x[j], f[kb + 1][s], fb[2], fb[3]);
+                }
+            }
+        }
+    }
+}
+
+// S += Z^T B for 8 N of the columns of S^T (from column 8 c0), Z in NT terms, B sixteen rows of a tile.
+template <int ROWB, int NT, int N>
+__device__ __forceinline__ void add_outer(float (&S)[N][4], const float (&z0)[4], const float (&z1)[4], uint32_t tile, int row,
+                                          int c0, int lane) {
+    uint32_t fs[NT][4];
+    split_a<NT>(z0, z1, fs);
+#pragma unroll
+    for (int nd = 0; nd < N / 2; ++nd) {
+        uint32_t fb[4];
+        ldsm_t(fb, tile + at<ROWB>(row + (lane & 15), c0 + 2 * nd + (lane >> 4)));
+#pragma unroll
+        for (int t = NT - 1; t >= 0; --t) {
+            mma(S[2 * nd], fs[t], fb[0], fb[1]);
+            mma(S[2 * nd + 1], fs[t], fb[2], fb[3]);
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void zero(float (&x)[N][4]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[n][j] = 0.f;
+}
+__device__ __forceinline__ float4 as4(const float (&x)[4]) { return make_float4(x[0], x[1], x[2], x[3]); }
+// Columns (rows of the chunk) of an accumulator tile times their factors.
+__device__ __forceinline__ void scale_cols(float (&x)[4], float2 f) {
+    x[0] *= f.x; x[1] *= f.y; x[2] *= f.x; x[3] *= f.y;
+}
+__device__ __forceinline__ float2 pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+
+template <int D, int NT, int SL, int MODE>
+__global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainArgs a) {
+    using L = ChainSmem<D, NT, SL, MODE>;
     using W = Chunk<NT>;
-    constexpr int DK = D / KS, OWN = 8 / KS, kAll = L::kAll;
+    constexpr int KS = L::KS, DK = D / KS, OWN = 8 / KS;
+    constexpr int kAll = 2 * kGroup + 32 * SL;           // the chain, the helpers at work, the loaders
     constexpr bool BACK = MODE == kBack;
     extern __shared__ __align__(128) char sm[];
-    const uint32_t sb = smem_u32(sm);
     const DeltaProblem &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bh = blockIdx.x / a.groups, grp = blockIdx.x % a.groups;
@@ -322,33 +390,36 @@ __global__ void __launch_bounds__(32 * SL * KS + kLoadThreads, 1) delta_chain_ke
     const int len = delta_len(p.lengths, b, p.N);
     const int nc = (len + C - 1) / C;
     const int c0 = grp * 16 * SL;                        // first column of the CTA
-    const size_t vrow = (size_t)bh * p.N, krow = ((size_t)b * p.Hk + hk) * p.N;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
+    const size_t vrow = (size_t)bh * p.N;
+    auto chunk_of = [&](int i) { return BACK ? nc - 1 - i : i; };
 
-    if (tid >= L::kThreads) {
-        if (L::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-        const int lt = tid - L::kThreads;
+    if (tid >= 2 * kGroup) {
+        // ---------------------------------------------------------------------------------------- loaders
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+        const int lt = tid - 2 * kGroup;
+        const uint32_t sb = smem_u32(sm);
+        const size_t krow = ((size_t)b * p.Hk + hk) * p.N;
         const __nv_bfloat16 *K = static_cast<const __nv_bfloat16 *>(p.Kx), *Q = static_cast<const __nv_bfloat16 *>(p.Qx);
         const __nv_bfloat16 *V = static_cast<const __nv_bfloat16 *>(p.V);
         auto load = [&](int i_th) {
             if (i_th < nc) {
-                const int c = BACK ? nc - 1 - i_th : i_th;
+                const int c = chunk_of(i_th);
                 const uint32_t st = sb + (i_th % L::kStages) * L::kStage;
-                for (int i = lt; i < C * (D / 8); i += kLoadThreads) {
+                for (int i = lt; i < C * (D / 8); i += kGroup) {
                     const int r = i / (D / 8), col = i % (D / 8), row = c * C + r;
                     const bool ok = row < len && col * 8 < p.d;
                     const size_t off = ok ? (krow + row) * p.d + col * 8 : 0;
                     copy16(st + at<L::kRow>(r, col), K + off, ok);
                     if (MODE != kCkpt) copy16(st + L::oQ + at<L::kRow>(r, col), Q + off, ok);
                 }
-                for (int i = lt; i < C * 2 * SL; i += kLoadThreads) {
+                for (int i = lt; i < C * 2 * SL; i += kGroup) {
                     const int r = i / (2 * SL), col = i % (2 * SL), row = c * C + r;
                     const bool ok = row < len && c0 + col * 8 < p.dv;
                     const size_t off = ok ? (vrow + row) * p.dv + c0 + col * 8 : 0;
                     copy16(st + L::oV + at<L::kValRow>(r, col), V + off, ok);
                 }
                 const char *ws = a.chunks + ((size_t)bh * a.nc + c) * W::bytes;
-                for (int i = lt; i < W::bytes / 16; i += kLoadThreads) copy16(st + L::oW + 16 * i, ws + 16 * i, true);
+                for (int i = lt; i < W::bytes / 16; i += kGroup) copy16(st + L::oW + 16 * i, ws + 16 * i, true);
             }
             copy_commit();
         };
@@ -362,15 +433,148 @@ __global__ void __launch_bounds__(32 * SL * KS + kLoadThreads, 1) delta_chain_ke
         }
         copy_wait<0>();
         if (MODE == kFwd) {                              // rows that do not exist
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
             const int w = min(16 * SL, p.dv - c0) / 8;
-            for (size_t i = lt; i < (size_t)(p.N - len) * w; i += kLoadThreads)
+            for (size_t i = lt; i < (size_t)(p.N - len) * w; i += kGroup)
                 *reinterpret_cast<uint4 *>(out + (vrow + len + i / w) * p.dv + c0 + (int)(i % w) * 8) = make_uint4(0, 0, 0, 0);
         }
         return;
     }
-    if (L::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kChainRegs));
-    const int slice = warp % SL, rank = KS > 1 ? warp / SL : 0;
-    const int col = c0 + 16 * slice + (lane >> 2), q0 = 2 * (lane & 3), k0 = rank * DK;
+    const int slice = warp % SL, rank = KS > 1 ? (warp % 4) / SL : 0;
+    char *mine = sm + L::oSlice + slice * L::kSlice;
+    float4 *sums = reinterpret_cast<float4 *>(mine);                                // [KS][8 tiles][32 lanes]
+    char *rows = mine + L::oRows;                                                   // R's terms; then U, [8 tiles][32 lanes]
+    uint4 *held = reinterpret_cast<uint4 *>(mine + L::oState);                      // the state: [D / 16][32 lanes]
+    float4 *zp = reinterpret_cast<float4 *>(mine + L::oZ), *zq = zp + 8 * 32;       // kBack
+    const int q0 = 2 * (lane & 3), br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;   // B operand: row, piece
+    const int col = c0 + 16 * slice + (lane >> 2);
+
+    if (tid >= kGroup) {
+        // ---------------------------------------------------------------------------------------- helpers
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHelpRegs));
+        if (warp - 4 >= SL) return;
+        // [16 columns, 64 rows] in packed pairs of rows as bf16 rows, through the chunk's own V columns, to memory
+        auto to_memory = [&](__nv_bfloat16 *to, int c, char *st, const uint32_t (&x)[8][2]) {
+#pragma unroll
+            for (int n = 0; n < 8; n += 2) {
+                const int r = 8 * n + br;
+                char *at_r = st + L::oV + at<L::kValRow>(r, 2 * slice + bc);
+                stsm_t(smem_u32(at_r), x[n][0], x[n][1], x[n + 1][0], x[n + 1][1]);
+                __syncwarp();
+                const int cc = c0 + 16 * slice + bc * 8, row = c * C + r;
+                if (row < len && cc < p.dv)
+                    *reinterpret_cast<uint4 *>(to + (vrow + row) * p.dv + cc) = *reinterpret_cast<const uint4 *>(at_r);
+            }
+            __syncwarp();
+        };
+        bar<kAll>(kBarAll);
+        for (int ci = 0; ci < nc; ++ci) {
+            const int c = chunk_of(ci);
+            char *st = sm + (ci % L::kStages) * L::kStage;
+            const uint32_t qt = smem_u32(st) + L::oQ, vt = smem_u32(st) + L::oV, pt = smem_u32(st) + L::oW + W::oP;
+            const Vec &vec = *reinterpret_cast<const Vec *>(st + L::oW + W::oVec);
+            float x[8][4];
+            zero(x);
+            if (MODE == kFwd) {
+                // O = scale e^G Q S, then + P U
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint4 s4 = held[ks * 32 + lane];
+                    const uint32_t fs[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                    for (int np = 0; np < 4; ++np) {
+                        uint32_t fq[4];
+                        ldsm(fq, qt + at<L::kRow>(np * 16 + br, 2 * ks + bc));
+                        mma(x[2 * np], fs, fq[0], fq[1]);
+                        mma(x[2 * np + 1], fs, fq[2], fq[3]);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const float2 e = pair(vec.e + 8 * n + q0);
+                    scale_cols(x[n], make_float2(p.scale * e.x, p.scale * e.y));
+                }
+            } else {
+                if (BACK) {
+                    // P^T dO, dO^T as the left operand; then (scale e^G dO)^T Q
+                    uint32_t fd[4][1][4];
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb) ldsm_t(fd[kb][0], vt + at<L::kValRow>(kb * 16 + br, 2 * slice + bc));
+                    triangle<true, 2, 1>(x, fd, pt, lane, [](int j) { return j; });
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) zp[n * 32 + lane] = as4(x[n]);
+                    bar<32 * (KS + 1)>(kBarZ + slice);
+                    float y[D / 8][4];
+                    zero(y);
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb) {
+                        float z[2][4];
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const float2 e = pair(vec.e + 16 * kb + 8 * m + q0);
+                            z[m][0] = low(fd[kb][0][2 * m]); z[m][1] = high(fd[kb][0][2 * m]);
+                            z[m][2] = low(fd[kb][0][2 * m + 1]); z[m][3] = high(fd[kb][0][2 * m + 1]);
+                            scale_cols(z[m], make_float2(p.scale * e.x, p.scale * e.y));
+                        }
+                        add_outer<L::kRow, NT>(y, z[0], z[1], qt, kb * 16, 0, lane);
+                    }
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) zq[n * 32 + lane] = as4(y[n]);
+                }
+                // the state as it is held: [dv, d] in bf16
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint4 s4 = held[ks * 32 + lane];
+                    const uint32_t s2[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const int r = 16 * ks + 8 * (m >> 1) + q0, cc = col + 8 * (m & 1);
+                        if (r < p.d && cc < p.dv)
+                            *reinterpret_cast<uint32_t *>(a.states + (((size_t)bh * a.nc + c) * p.dv + cc) * p.d + r) = s2[m];
+                    }
+                }
+            }
+            bar<32 * (KS + 1)>(kBarU + slice);           // U is there; the chain may change `held`
+            float z[8][4];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const float4 y = reinterpret_cast<const float4 *>(rows)[n * 32 + lane];
+                z[n][0] = y.x; z[n][1] = y.y; z[n][2] = y.z; z[n][3] = y.w;
+            }
+            if (MODE == kFwd) {
+                uint32_t fu[4][2][4], o[8][2];
+#pragma unroll
+                for (int kb = 0; kb < 4; ++kb) split_a<2>(z[2 * kb], z[2 * kb + 1], fu[kb]);
+                triangle<false, 2, 1>(x, fu, pt, lane, [](int j) { return j; });
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    o[n][0] = pack(x[n][0], x[n][1]);
+                    o[n][1] = pack(x[n][2], x[n][3]);
+                }
+                to_memory(static_cast<__nv_bfloat16 *>(a.out), c, st, o);
+            } else {
+                // W = U / beta (X as it is) in two terms
+                uint32_t t0[8][2], t1[8][2];
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    if (!BACK) scale_cols(z[n], pair(vec.ibeta + 8 * n + q0));
+                    uint32_t t[2];
+                    split<2>(z[n][0], z[n][1], t);
+                    t0[n][0] = t[0]; t1[n][0] = t[1];
+                    split<2>(z[n][2], z[n][3], t);
+                    t0[n][1] = t[0]; t1[n][1] = t[1];
+                }
+                to_memory(a.rows, c, st, t0);
+                to_memory(a.rows + (size_t)p.B * p.H * p.N * p.dv, c, st, t1);
+            }
+            bar<kAll>(kBarAll);
+        }
+        return;
+    }
+
+    // -------------------------------------------------------------------------------------------- the chain
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChainRegs));
+    const int k0 = rank * DK;
     const size_t sbase = (size_t)bh * p.d * p.dv;
     float S[DK / 8][4];                                  // S^T: rows col, col + 8; columns k0 + 8 n + q0, + 1
 #pragma unroll
@@ -380,221 +584,68 @@ __global__ void __launch_bounds__(32 * SL * KS + kLoadThreads, 1) delta_chain_ke
             const int r = k0 + 8 * n + q0 + (j & 1), cc = col + 8 * (j >> 1);
             S[n][j] = a.state_in && r < p.d && cc < p.dv ? a.state_in[sbase + (size_t)r * p.dv + cc] : 0.f;
         }
-    const int br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;              // B operand: rows n, pieces k
-    const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, tc = lane >> 4;              // transposed: rows k, pieces n
+    auto hold = [&] {
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks)
+            held[(k0 / 16 + ks) * 32 + lane] = make_uint4(pack(S[2 * ks][0], S[2 * ks][1]), pack(S[2 * ks][2], S[2 * ks][3]),
+                                                          pack(S[2 * ks + 1][0], S[2 * ks + 1][1]),
+                                                          pack(S[2 * ks + 1][2], S[2 * ks + 1][3]));
+    };
     // the warp's eight-row tiles: all, or r, 7 - r (and r + 2, 5 - r of two warps)
     auto own = [&](int j) {
         return KS == 1 ? j : j == 0 ? rank : j == 1 ? 7 - rank : j == 2 ? rank + 2 : 5 - rank;
     };
-    float4 *sums = reinterpret_cast<float4 *>(sm + L::oSum + slice * L::kSum);      // [KS][8 tiles][32 lanes]
-    char *rows = sm + L::oRows + slice * L::kRows;
     auto meet = [&] { if (KS > 1) bar<32 * KS>(kBarSlice + slice); };
-    auto put_sums = [&](const float (&x)[8][4]) {
-        if (KS > 1)
-#pragma unroll
-            for (int n = 0; n < 8; ++n) sums[(rank * 8 + n) * 32 + lane] = make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
-    };
-    auto get_sums = [&](const float (&all)[8][4], float (&x)[OWN][4]) {
-#pragma unroll
-        for (int j = 0; j < OWN; ++j) {
-            if (KS == 1) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) x[j][m] = all[j][m];
-            } else {
-                const int n = own(j);
-                float4 y = sums[n * 32 + lane];
-#pragma unroll
-                for (int k = 1; k < KS; ++k) {
-                    const float4 z = sums[(k * 8 + n) * 32 + lane];
-                    y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
-                }
-                x[j][0] = y.x; x[j][1] = y.y; x[j][2] = y.z; x[j][3] = y.w;
-            }
-        }
-    };
-    // the A operand's terms of all 64 rows from each warp's tiles
-    auto offer_terms = [&](const float (&x)[OWN][4]) {
-        if (KS > 1)
-#pragma unroll
-            for (int j = 0; j < OWN; ++j) {
-                uint32_t t0[NT], t1[NT];
-                split<NT>(x[j][0], x[j][1], t0);
-                split<NT>(x[j][2], x[j][3], t1);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    reinterpret_cast<uint2 *>(rows)[(t * 8 + own(j)) * 32 + lane] = make_uint2(t0[t], t1[t]);
-            }
-    };
-    auto take_terms = [&](const float (&x)[OWN][4], uint32_t (&f)[4][NT][4]) {
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-            if (KS == 1) {
-                split_a<NT>(x[(2 * kb) % OWN], x[(2 * kb + 1) % OWN], f[kb]);
-            } else {
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const uint2 u0 = reinterpret_cast<const uint2 *>(rows)[(t * 8 + 2 * kb) * 32 + lane];
-                    const uint2 u1 = reinterpret_cast<const uint2 *>(rows)[(t * 8 + 2 * kb + 1) * 32 + lane];
-                    f[kb][t][0] = u0.x; f[kb][t][1] = u0.y; f[kb][t][2] = u1.x; f[kb][t][3] = u1.y;
-                }
-            }
-        }
-    };
-    auto share = [&](const float (&x)[OWN][4], float (&z)[8][4]) {
-        if (KS > 1) {
-#pragma unroll
-            for (int j = 0; j < OWN; ++j)
-                reinterpret_cast<float4 *>(rows)[own(j) * 32 + lane] = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
-            meet();
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            float4 y;
-            if (KS == 1) y = make_float4(x[n % OWN][0], x[n % OWN][1], x[n % OWN][2], x[n % OWN][3]);
-            else y = reinterpret_cast<const float4 *>(rows)[n * 32 + lane];
-            z[n][0] = y.x; z[n][1] = y.y; z[n][2] = y.z; z[n][3] = y.w;
-        }
-    };
-    // x += F^T M^T (BACK: F^T M) for the warp's tiles, M a packed triangle: FT terms of F, TT of M, their products up to
-    // MOST in the terms' sum
-    auto triangle = [&](auto &x, const auto &f, uint32_t t0, auto ft, auto tt, auto most) {
-        constexpr int FT = decltype(ft)::value, TT = decltype(tt)::value, MOST = decltype(most)::value;
-#pragma unroll
-        for (int j = 0; j < OWN; ++j) {
-            const int n = own(j), nb = n >> 1;
-#pragma unroll
-            for (int kb = 0; kb < 4; kb += 2) {
-                // blocks kb and kb + 1 along the sum; one outside the triangle is read as its neighbour and not used
-                const bool one = BACK ? kb >= nb : kb <= nb, two = BACK ? kb + 1 >= nb : kb + 1 <= nb;
-                if (!one && !two) continue;
-                const int k = kb + (lane >> 4);
-                const uint32_t blk = t0 + (BACK ? tri(max(k, nb), nb) + at<32>(lane & 15, n & 1)
-                                                : tri(nb, min(k, nb)) + at<32>((n & 1) * 8 + (lane & 7), bc));
-#pragma unroll
-                for (int t = TT - 1; t >= 0; --t) {
-                    uint32_t fb[4];
-                    if (BACK) ldsm_t(fb, blk + t * kTriBytes);
-                    else ldsm(fb, blk + t * kTriBytes);
-#pragma unroll
-                    for (int s = FT - 1; s >= 0; --s) {
-                        if (s + t > MOST) continue;
-                        if (one) mma(x[j], f[kb][s], fb[0], fb[1]);
-                        if (two) mma(x[j], f[kb + 1][s], fb[2], fb[3]);
-                    }
-                }
-            }
-        }
-    };
-    // the warp's tiles [16 columns, 8 rows] as bf16 rows through the chunk's own V columns to memory
-    auto to_memory = [&](__nv_bfloat16 *to, int c, char *st, auto tile) {
-#pragma unroll
-        for (int j = 0; j < OWN; j += 2) {
-            const int r = (lane >> 4 ? own(j + 1) : own(j)) * 8 + (lane & 7);
-            char *mine = st + L::oV + at<L::kValRow>(r, 2 * slice + bc);
-            uint32_t x[2], y[2];
-            tile(j, x);
-            tile(j + 1, y);
-            stsm_t(smem_u32(mine), x[0], x[1], y[0], y[1]);
-            __syncwarp();
-            const int cc = c0 + 16 * slice + bc * 8, row = c * C + r;
-            if (row < len && cc < p.dv)
-                *reinterpret_cast<uint4 *>(to + (vrow + row) * p.dv + cc) = *reinterpret_cast<const uint4 *>(mine);
-        }
-    };
-    // S += Z^T B for the warp's columns, Z in NT terms, B the rows of a tile
-    auto add_outer = [&](const float (&z0)[4], const float (&z1)[4], int kb, uint32_t tile) {
-        uint32_t fs[NT][4];
-        split_a<NT>(z0, z1, fs);
-#pragma unroll
-        for (int nd = 0; nd < DK / 16; ++nd) {
-            uint32_t fb[4];
-            ldsm_t(fb, tile + at<L::kRow>(kb * 16 + tr, k0 / 8 + 2 * nd + tc));
-#pragma unroll
-            for (int t = NT - 1; t >= 0; --t) {
-                mma(S[2 * nd], fs[t], fb[0], fb[1]);
-                mma(S[2 * nd + 1], fs[t], fb[2], fb[3]);
-            }
-        }
-    };
+    hold();
     bar<kAll>(kBarAll);
     for (int ci = 0; ci < nc; ++ci) {
-        const int c = BACK ? nc - 1 - ci : ci;
-        char *st = sm + (ci % L::kStages) * L::kStage;
-        const uint32_t kt = smem_u32(st), qt = kt + L::oQ, vt = kt + L::oV, tt = kt + L::oW, pt = tt + W::oP;
+        const char *st = sm + (ci % L::kStages) * L::kStage;
+        const uint32_t kt = smem_u32(st), vt = kt + L::oV, tt = kt + L::oW;
         const Vec &vec = *reinterpret_cast<const Vec *>(st + L::oW + W::oVec);
-        if (MODE != kFwd) {
-            // the state as it is held: [dv, d] in bf16
-#pragma unroll
-            for (int n = 0; n < DK / 8; ++n)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int r = k0 + 8 * n + q0, cc = col + 8 * j;
-                    if (r < p.d && cc < p.dv)
-                        *reinterpret_cast<uint32_t *>(a.states + (((size_t)bh * a.nc + c) * p.dv + cc) * p.d + r) =
-                            pack(S[n][2 * j], S[n][2 * j + 1]);
-                }
-        }
-        // y = (K S)^T in NT terms of S; kFwd: o = (Q S)^T in one.  This warp's part of the sum over d.
-        float y[8][4], o[8][4];
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[n][j] = o[n][j] = 0.f;
+        // y = (K S)^T in NT terms of S: this warp's part of the sum over d
+        float y[8][4];
+        zero(y);
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
             uint32_t fs[NT][4];
             split_a<NT>(S[2 * ks], S[2 * ks + 1], fs);
 #pragma unroll
             for (int np = 0; np < 4; ++np) {
-                uint32_t fb[4], fq[4];
+                uint32_t fb[4];
                 ldsm(fb, kt + at<L::kRow>(np * 16 + br, k0 / 8 + 2 * ks + bc));
-                if (MODE == kFwd) ldsm(fq, qt + at<L::kRow>(np * 16 + br, k0 / 8 + 2 * ks + bc));
 #pragma unroll
                 for (int t = NT - 1; t >= 0; --t) {
                     mma(y[2 * np], fs[t], fb[0], fb[1]);
                     mma(y[2 * np + 1], fs[t], fb[2], fb[3]);
                 }
-                if (MODE == kFwd) {
-                    mma(o[2 * np], fs[0], fq[0], fq[1]);
-                    mma(o[2 * np + 1], fs[0], fq[2], fq[3]);
-                }
             }
         }
-        put_sums(y);
-        const float last = vec.last;
-#pragma unroll
-        for (int n = 0; n < DK / 8; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) S[n][j] *= last;
-        uint32_t fd[4][1][4];                            // kBack: dO^T as the left operand
-        if (BACK) {
-            // what does not wait for y: R += (scale e^G dO)^T Q
-#pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-                ldsm_t(fd[kb][0], vt + at<L::kValRow>(kb * 16 + br, 2 * slice + bc));
-                float z[2][4];
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const float2 e = *reinterpret_cast<const float2 *>(vec.e + 16 * kb + 8 * m + q0);
-                    const float ex = p.scale * e.x, ey = p.scale * e.y;
-                    z[m][0] = ex * low(fd[kb][0][2 * m]); z[m][1] = ey * high(fd[kb][0][2 * m]);
-                    z[m][2] = ex * low(fd[kb][0][2 * m + 1]); z[m][3] = ey * high(fd[kb][0][2 * m + 1]);
-                }
-                add_outer(z[0], z[1], kb, qt);
-            }
-        }
-        meet();
         float x[OWN][4];
-        get_sums(y, x);
+        if (KS > 1) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) sums[(rank * 8 + n) * 32 + lane] = as4(y[n]);
+            meet();
+        }
+#pragma unroll
+        for (int j = 0; j < OWN; ++j) {
+            float4 s4 = KS > 1 ? sums[own(j) * 32 + lane] : as4(y[j]);
+#pragma unroll
+            for (int k = 1; k < KS; ++k) {
+                const float4 z = sums[(k * 8 + own(j)) * 32 + lane];
+                s4.x += z.x; s4.y += z.y; s4.z += z.z; s4.w += z.w;
+            }
+            x[j][0] = s4.x; x[j][1] = s4.y; x[j][2] = s4.z; x[j][3] = s4.w;
+        }
         if (BACK) {
             // dU = f K R + P^T dO
+            bar<32 * (KS + 1)>(kBarZ + slice);
 #pragma unroll
             for (int j = 0; j < OWN; ++j) {
-                const float2 f = *reinterpret_cast<const float2 *>(vec.f + 8 * own(j) + q0);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) x[j][m] *= (m & 1) ? f.y : f.x;
+                const float2 f = pair(vec.f + 8 * own(j) + q0);
+                const float4 z = zp[own(j) * 32 + lane];
+                x[j][0] = fmaf(f.x, x[j][0], z.x); x[j][1] = fmaf(f.y, x[j][1], z.y);
+                x[j][2] = fmaf(f.x, x[j][2], z.z); x[j][3] = fmaf(f.y, x[j][3], z.w);
             }
-            triangle(x, fd, pt, Int<1>{}, Int<2>{}, Int<1>{});
         } else {
             // R = beta (V - e^G K S)
 #pragma unroll
@@ -603,8 +654,7 @@ __global__ void __launch_bounds__(32 * SL * KS + kLoadThreads, 1) delta_chain_ke
                 ldsm_t(fv, vt + at<L::kValRow>((lane >> 4 ? own(j + 1) : own(j)) * 8 + (lane & 7), 2 * slice + bc));
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    const float2 e = *reinterpret_cast<const float2 *>(vec.e + 8 * own(j + m) + q0);
-                    const float2 be = *reinterpret_cast<const float2 *>(vec.beta + 8 * own(j + m) + q0);
+                    const float2 e = pair(vec.e + 8 * own(j + m) + q0), be = pair(vec.beta + 8 * own(j + m) + q0);
                     x[j + m][0] = be.x * fmaf(-e.x, x[j + m][0], low(fv[2 * m]));
                     x[j + m][1] = be.y * fmaf(-e.y, x[j + m][1], high(fv[2 * m]));
                     x[j + m][2] = be.x * fmaf(-e.x, x[j + m][2], low(fv[2 * m + 1]));
@@ -614,64 +664,63 @@ __global__ void __launch_bounds__(32 * SL * KS + kLoadThreads, 1) delta_chain_ke
         }
         // U = T R (kBack: X = T^T dU)
         uint32_t fr[4][NT][4];
-        offer_terms(x);
-        meet();
-        if (MODE == kFwd) put_sums(o);
-        take_terms(x, fr);
-        meet();
-#pragma unroll
-        for (int j = 0; j < OWN; ++j)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) x[j][m] = 0.f;
-        triangle(x, fr, tt, Int<NT>{}, Int<NT>{}, Int<NT - 1>{});
-        if (MODE != kFwd) {
-            // W (X) in two bf16 terms through the chunk's own V columns to memory
-            uint32_t t0[OWN][2], t1[OWN][2];
+        if (KS > 1) {
 #pragma unroll
             for (int j = 0; j < OWN; ++j) {
-                const float2 ib = *reinterpret_cast<const float2 *>(vec.ibeta + 8 * own(j) + q0);
-                const float2 be = *reinterpret_cast<const float2 *>(vec.beta + 8 * own(j) + q0);
-                split<2>(BACK ? x[j][0] : x[j][0] * ib.x, BACK ? x[j][1] : x[j][1] * ib.y, t0[j]);
-                split<2>(BACK ? x[j][2] : x[j][2] * ib.x, BACK ? x[j][3] : x[j][3] * ib.y, t1[j]);
-                if (BACK)
+                uint32_t t0[NT], t1[NT];
+                split<NT>(x[j][0], x[j][1], t0);
+                split<NT>(x[j][2], x[j][3], t1);
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) x[j][m] *= (m & 1) ? -be.y : -be.x;
+                for (int t = 0; t < NT; ++t)
+                    reinterpret_cast<uint2 *>(rows)[(t * 8 + own(j)) * 32 + lane] = make_uint2(t0[t], t1[t]);
             }
+            meet();
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                __syncwarp();
-                to_memory(a.rows + t * (size_t)p.B * p.H * p.N * p.dv, c, st,
-                          [&](int j, uint32_t (&r)[2]) { r[0] = t0[j][t]; r[1] = t1[j][t]; });
-            }
+            for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint2 u0 = reinterpret_cast<const uint2 *>(rows)[(t * 8 + 2 * kb) * 32 + lane];
+                    const uint2 u1 = reinterpret_cast<const uint2 *>(rows)[(t * 8 + 2 * kb + 1) * 32 + lane];
+                    fr[kb][t][0] = u0.x; fr[kb][t][1] = u0.y; fr[kb][t][2] = u1.x; fr[kb][t][3] = u1.y;
+                }
+            meet();
+        } else {
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) split_a<NT>(x[(2 * kb) % OWN], x[(2 * kb + 1) % OWN], fr[kb]);
         }
-        float z[8][4];
-        share(x, z);
-        if (MODE == kFwd) {
-            // O = scale e^G Q S + P U
-            uint32_t fu[4][2][4];
+        zero(x);
+        triangle<BACK, NT, NT - 1>(x, fr, tt, lane, own);
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb) split_a<2>(z[2 * kb], z[2 * kb + 1], fu[kb]);
-            get_sums(o, x);
+        for (int j = 0; j < OWN; ++j) reinterpret_cast<float4 *>(rows)[own(j) * 32 + lane] = as4(x[j]);
+        bar<32 * (KS + 1)>(kBarU + slice);
+        // S <- e^{G_C} S + (f U)^T K  (kBack: R <- e^{G_C} R + the helper's part - (e^G beta X)^T K)
+        const float last = vec.last;
 #pragma unroll
-            for (int j = 0; j < OWN; ++j) {
-                const float2 e = *reinterpret_cast<const float2 *>(vec.e + 8 * own(j) + q0);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) x[j][m] *= p.scale * ((m & 1) ? e.y : e.x);
-            }
-            triangle(x, fu, pt, Int<2>{}, Int<2>{}, Int<1>{});
-            to_memory(out, c, st, [&](int j, uint32_t (&r)[2]) { r[0] = pack(x[j][0], x[j][1]); r[1] = pack(x[j][2], x[j][3]); });
+        for (int n = 0; n < DK / 8; ++n) {
+            const float4 z = BACK ? zq[(k0 / 8 + n) * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[n][0] = BACK ? fmaf(last, S[n][0], z.x) : last * S[n][0];
+            S[n][1] = BACK ? fmaf(last, S[n][1], z.y) : last * S[n][1];
+            S[n][2] = BACK ? fmaf(last, S[n][2], z.z) : last * S[n][2];
+            S[n][3] = BACK ? fmaf(last, S[n][3], z.w) : last * S[n][3];
         }
-        // S += (f U)^T K  (kBack: R -= (e^G beta X)^T K)
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
+            float z[2][4];
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                const float2 f = *reinterpret_cast<const float2 *>((BACK ? vec.e : vec.f) + 16 * kb + 8 * m + q0);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) z[2 * kb + m][j] *= (j & 1) ? f.y : f.x;
+                const int n = 2 * kb + m;
+                const float4 u = KS > 1 ? reinterpret_cast<const float4 *>(rows)[n * 32 + lane] : as4(x[n % OWN]);
+                z[m][0] = u.x; z[m][1] = u.y; z[m][2] = u.z; z[m][3] = u.w;
+                float2 f = pair((BACK ? vec.e : vec.f) + 8 * n + q0);
+                if (BACK) {
+                    const float2 be = pair(vec.beta + 8 * n + q0);
+                    f.x *= -be.x; f.y *= -be.y;
+                }
+                scale_cols(z[m], f);
             }
-            add_outer(z[2 * kb], z[2 * kb + 1], kb, kt);
+            add_outer<L::kRow, NT>(S, z[0], z[1], kt, kb * 16, k0 / 8, lane);
         }
+        hold();
         bar<kAll>(kBarAll);
     }
     if (a.state_out)
@@ -693,21 +742,23 @@ cudaError_t prep(const DeltaProblem &p, char *chunks, bool held, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <int D, int NT, int SL, int KS, int MODE>
+template <int D, int NT, int SL, int MODE>
 cudaError_t chain(ChainArgs a, cudaStream_t s) {
-    using L = ChainSmem<D, NT, SL, KS>;
+    using L = ChainSmem<D, NT, SL, MODE>;
     a.groups = (a.p.dv + 16 * SL - 1) / (16 * SL);
-    const cudaError_t e = set_dyn_smem((const void *)delta_chain_kernel<D, NT, SL, KS, MODE>, L::total);
+    const cudaError_t e = set_dyn_smem((const void *)delta_chain_kernel<D, NT, SL, MODE>, L::total);
     if (e != cudaSuccess) return e;
-    delta_chain_kernel<D, NT, SL, KS, MODE><<<(unsigned)(a.p.B * a.p.H * a.groups), L::kAll, L::total, s>>>(a);
+    delta_chain_kernel<D, NT, SL, MODE><<<(unsigned)(a.p.B * a.p.H * a.groups), 3 * kGroup, L::total, s>>>(a);
     return cudaGetLastError();
 }
 
+// One CTA to an SM, four chain warps to a CTA: as many of them to 16 columns as one wave of CTAs allows.
 template <int D, int NT, int MODE>
 cudaError_t chains(const ChainArgs &a, cudaStream_t s) {
     const long long heads = (long long)a.p.B * a.p.H;
-    if (heads * ((a.p.dv + 31) / 32) <= 152) return chain<D, NT, 2, 4, MODE>(a, s);
-    return chain<D, NT, 4, 1, MODE>(a, s);
+    if (heads * ((a.p.dv + 15) / 16) <= 152) return chain<D, NT, 1, MODE>(a, s);
+    if (heads * ((a.p.dv + 31) / 32) <= 152) return chain<D, NT, 2, MODE>(a, s);
+    return chain<D, NT, 4, MODE>(a, s);
 }
 
 }  // namespace
