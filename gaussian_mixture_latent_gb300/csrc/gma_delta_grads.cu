@@ -119,16 +119,19 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
             uint32_t f[2][4];
             ldsm(f[0], left + at<128>(rb * 16 + ar, 2 * ks + ac));
             if (role) ldsm(f[1], left + L::kSlab + at<128>(rb * 16 + ar, 2 * ks + ac));
+            // four tiles of one term, then of the other: an accumulator is used again after three other products
 #pragma unroll
-            for (int nd = 0; nd < D / 16; ++nd) {
-                uint32_t g[4];
-                ldsm_t(g, st + at<L::kRow>(ks * 16 + ar, 2 * nd + ac));
-                if (role) {
-                    mma(acc[2 * nd], f[1], g[0], g[1]);
-                    mma(acc[2 * nd + 1], f[1], g[2], g[3]);
-                }
-                mma(acc[2 * nd], f[0], g[0], g[1]);
-                mma(acc[2 * nd + 1], f[0], g[2], g[3]);
+            for (int nd = 0; nd < D / 16; nd += 2) {
+                uint32_t g[2][4];
+                ldsm_t(g[0], st + at<L::kRow>(ks * 16 + ar, 2 * nd + ac));
+                ldsm_t(g[1], st + at<L::kRow>(ks * 16 + ar, 2 * nd + 2 + ac));
+#pragma unroll
+                for (int t = role ? 1 : 0; t >= 0; --t)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        mma(acc[2 * (nd + m)], f[t], g[m][0], g[m][1]);
+                        mma(acc[2 * (nd + m) + 1], f[t], g[m][2], g[m][3]);
+                    }
             }
         }
     };
@@ -313,14 +316,17 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
                     for (int m = 0; m < 4; ++m) f[t][m] ^= 0x80008000u;
             }
 #pragma unroll
-            for (int nd = 0; nd < D / 16; ++nd) {
-                uint32_t g[4];
-                ldsm_t(g, right + at<L::kRow>(kb * 16 + ar, 2 * nd + ac));
+            for (int nd = 0; nd < D / 16; nd += 2) {
+                uint32_t g[2][4];
+                ldsm_t(g[0], right + at<L::kRow>(kb * 16 + ar, 2 * nd + ac));
+                ldsm_t(g[1], right + at<L::kRow>(kb * 16 + ar, 2 * nd + 2 + ac));
 #pragma unroll
-                for (int t = 1; t >= 0; --t) {
-                    mma(acc[2 * nd], f[t], g[0], g[1]);
-                    mma(acc[2 * nd + 1], f[t], g[2], g[3]);
-                }
+                for (int t = 1; t >= 0; --t)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        mma(acc[2 * (nd + m)], f[t], g[m][0], g[m][1]);
+                        mma(acc[2 * (nd + m) + 1], f[t], g[m][2], g[m][3]);
+                    }
             }
         }
     };

@@ -15,6 +15,8 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// Volatile: where a warp is alone on its tensor unit, what else it has to do stands between the products in the source,
+// and it stays there (the unit takes one product each eight cycles, and a warp issues in order).
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -22,13 +24,14 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Volatile, so that they stay between the barriers they stand between, but without a claim on other memory.
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
 }
 __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
 }
 __device__ __forceinline__ void stsm_t(uint32_t at, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
@@ -48,7 +51,7 @@ __device__ __forceinline__ void bar(int id) { asm volatile("bar.sync %0, %1;" ::
 
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 __device__ __forceinline__ float low(uint32_t x) { return __uint_as_float(x << 16); }
@@ -68,22 +71,19 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&t)[NT]) {
     }
 }
 
-// The A operand's terms (16 rows x 16 k) from two neighbouring accumulator tiles of 16 x 8.
+// Quarter q of the A operand's terms (16 rows x 16 k) from two neighbouring accumulator tiles of 16 x 8.
+template <int NT>
+__device__ __forceinline__ void split_quarter(const float (&c0)[4], const float (&c1)[4], uint32_t (&a)[NT][4], int q) {
+    uint32_t t[NT];
+    if (q < 2) split<NT>(c0[2 * (q & 1)], c0[2 * (q & 1) + 1], t);
+    else split<NT>(c1[2 * (q & 1)], c1[2 * (q & 1) + 1], t);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) a[i][q] = t[i];
+}
 template <int NT>
 __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], uint32_t (&a)[NT][4]) {
-    uint32_t t[NT];
-    split<NT>(c0[0], c0[1], t);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) a[i][0] = t[i];
-    split<NT>(c0[2], c0[3], t);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) a[i][1] = t[i];
-    split<NT>(c1[0], c1[1], t);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) a[i][2] = t[i];
-    split<NT>(c1[2], c1[3], t);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) a[i][3] = t[i];
+    for (int q = 0; q < 4; ++q) split_quarter<NT>(c0, c1, a, q);
 }
 
 // Byte offset of 16-byte piece `c` of row `r` in a tile of ROWB-byte rows (32, 64, 128, 256): pieces are exchanged so

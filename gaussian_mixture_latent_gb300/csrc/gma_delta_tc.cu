@@ -312,52 +312,76 @@ struct ChainSmem {
 };
 
 // x += F^T M^T (BACK: F^T M) for N eight-row tiles tile(j), M a packed triangle at t0: FT terms of F, TT of M, and of
-// their products those whose terms' indexes sum to MOST at most.
-template <bool BACK, int TT, int MOST, int N, int FT, class Tile>
-__device__ __forceinline__ void triangle(float (&x)[N][4], const uint32_t (&f)[4][FT][4], uint32_t t0, int lane, Tile tile) {
+// their products those whose terms' indexes sum to MOST at most.  unit(0..3) is called in between, before F's later half
+// of the sum (BACK: its earlier half) is used.
+template <bool BACK, int TT, int MOST, int N, int FT, class Tile, class Unit>
+__device__ __forceinline__ void triangle(float (&x)[N][4], const uint32_t (&f)[4][FT][4], uint32_t t0, int lane, Tile tile,
+                                         Unit unit) {
     const int bc = (lane >> 3) & 1;
+    int units = 0;
+    // the tiles are innermost: an accumulator is used again after as many other products as there are tiles
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int n = tile(j), nb = n >> 1;
+    for (int half = 0; half < 2; ++half) {
+        const int kb = BACK ? 2 - 2 * half : 2 * half;
 #pragma unroll
-        for (int kb = 0; kb < 4; kb += 2) {
+        for (int t = TT - 1; t >= 0; --t) {
             // blocks kb and kb + 1 along the sum; one outside the triangle is read as its neighbour and not used
-            const bool one = BACK ? kb >= nb : kb <= nb, two = BACK ? kb + 1 >= nb : kb + 1 <= nb;
-            if (!one && !two) continue;
-            const int k = kb + (lane >> 4);
-            const uint32_t blk = t0 + (BACK ? tri(max(k, nb), nb) + at<32>(lane & 15, n & 1)
-                                            : tri(nb, min(k, nb)) + at<32>((n & 1) * 8 + (lane & 7), bc));
+            uint32_t fb[N][4];
+            bool one[N], two[N];
 #pragma unroll
-            for (int t = TT - 1; t >= 0; --t) {
-                uint32_t fb[4];
-                if (BACK) ldsm_t(fb, blk + t * kTriBytes);
-                else ldsm(fb, blk + t * kTriBytes);
+            for (int j = 0; j < N; ++j) {
+                const int n = tile(j), nb = n >> 1, k = kb + (lane >> 4);
+                one[j] = BACK ? kb >= nb : kb <= nb;
+                two[j] = BACK ? kb + 1 >= nb : kb + 1 <= nb;
+                if (!one[j] && !two[j]) continue;
+                if (BACK) ldsm_t(fb[j], t0 + t * kTriBytes + tri(max(k, nb), nb) + at<32>(lane & 15, n & 1));
+                else ldsm(fb[j], t0 + t * kTriBytes + tri(nb, min(k, nb)) + at<32>((n & 1) * 8 + (lane & 7), bc));
+            }
 #pragma unroll
-                for (int s = FT - 1; s >= 0; --s) {
-                    if (s + t > MOST) continue;
-                    if (one) mma(x[j], f[kb][s], fb[0], fb[1]);
-                    if (two) mma(x[j], f[kb + 1][s], fb[2], fb[3]);
+            for (int s = FT - 1; s >= 0; --s) {
+                if (s + t > MOST) continue;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    if (one[j]) mma(x[j], f[kb][s], fb[j][0], fb[j][1]);
+                    if (j % 2 && units < 4) unit(units++);
                 }
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (two[j]) mma(x[j], f[kb + 1][s], fb[j][2], fb[j][3]);
             }
         }
     }
 }
 
-// S += Z^T B for 8 N of the columns of S^T (from column 8 c0), Z in NT terms, B sixteen rows of a tile.
-template <int ROWB, int NT, int N>
-__device__ __forceinline__ void add_outer(float (&S)[N][4], const float (&z0)[4], const float (&z1)[4], uint32_t tile, int row,
-                                          int c0, int lane) {
-    uint32_t fs[NT][4];
-    split_a<NT>(z0, z1, fs);
+// S += sum over the four blocks kb of Z_kb^T B_kb, for 8 N of the columns of S^T (from column 8 c0): Z in NT terms, from
+// get(kb, z0, z1), B_kb sixteen rows of a tile.  The next block's terms are made between the products.
+template <int ROWB, int NT, int N, class Get>
+__device__ __forceinline__ void add_outer(float (&S)[N][4], uint32_t tile, int c0, int lane, Get get) {
+    uint32_t fs[2][NT][4], fb[2][N / 2][4];
+    float z0[4], z1[4];
+    auto right = [&](int kb, int nd) {
+        ldsm_t(fb[kb & 1][nd], tile + at<ROWB>(kb * 16 + (lane & 15), c0 + 2 * nd + (lane >> 4)));
+    };
 #pragma unroll
-    for (int nd = 0; nd < N / 2; ++nd) {
-        uint32_t fb[4];
-        ldsm_t(fb, tile + at<ROWB>(row + (lane & 15), c0 + 2 * nd + (lane >> 4)));
+    for (int nd = 0; nd < N / 2; ++nd) right(0, nd);
+    get(0, z0, z1);
+    split_a<NT>(z0, z1, fs[0]);
 #pragma unroll
-        for (int t = NT - 1; t >= 0; --t) {
-            mma(S[2 * nd], fs[t], fb[0], fb[1]);
-            mma(S[2 * nd + 1], fs[t], fb[2], fb[3]);
-        }
+    for (int kb = 0; kb < 4; ++kb) {
+        if (kb < 3) get(kb + 1, z0, z1);
+        int q = 0;
+#pragma unroll
+        for (int t = NT - 1; t >= 0; --t)
+#pragma unroll
+            for (int nd = 0; nd < N / 2; ++nd) {
+                mma(S[2 * nd], fs[kb & 1][t], fb[kb & 1][nd][0], fb[kb & 1][nd][1]);
+                mma(S[2 * nd + 1], fs[kb & 1][t], fb[kb & 1][nd][2], fb[kb & 1][nd][3]);
+                if (kb < 3 && t == NT - 1) right(kb + 1, nd);
+                if (kb < 3 && q < 4) split_quarter<NT>(z0, z1, fs[(kb + 1) & 1], q++);
+            }
+#pragma unroll
+        for (; q < 4; ++q)
+            if (kb < 3) split_quarter<NT>(z0, z1, fs[(kb + 1) & 1], q);
     }
 }
 
@@ -474,6 +498,7 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             const uint32_t qt = smem_u32(st) + L::oQ, vt = smem_u32(st) + L::oV, pt = smem_u32(st) + L::oW + W::oP;
             const Vec &vec = *reinterpret_cast<const Vec *>(st + L::oW + W::oVec);
             float x[8][4];
+            uint4 was[D / 16];
             zero(x);
             if (MODE == kFwd) {
                 // O = scale e^G Q S, then + P U
@@ -500,39 +525,25 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
                     uint32_t fd[4][1][4];
 #pragma unroll
                     for (int kb = 0; kb < 4; ++kb) ldsm_t(fd[kb][0], vt + at<L::kValRow>(kb * 16 + br, 2 * slice + bc));
-                    triangle<true, 2, 1>(x, fd, pt, lane, [](int j) { return j; });
+                    triangle<true, 2, 1>(x, fd, pt, lane, [](int j) { return j; }, [](int) {});
 #pragma unroll
                     for (int n = 0; n < 8; ++n) zp[n * 32 + lane] = as4(x[n]);
                     bar<32 * (KS + 1)>(kBarZ + slice);
                     float y[D / 8][4];
                     zero(y);
-#pragma unroll
-                    for (int kb = 0; kb < 4; ++kb) {
-                        float z[2][4];
-#pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            const float2 e = pair(vec.e + 16 * kb + 8 * m + q0);
-                            z[m][0] = low(fd[kb][0][2 * m]); z[m][1] = high(fd[kb][0][2 * m]);
-                            z[m][2] = low(fd[kb][0][2 * m + 1]); z[m][3] = high(fd[kb][0][2 * m + 1]);
-                            scale_cols(z[m], make_float2(p.scale * e.x, p.scale * e.y));
-                        }
-                        add_outer<L::kRow, NT>(y, z[0], z[1], qt, kb * 16, 0, lane);
-                    }
+                    add_outer<L::kRow, NT>(y, qt, 0, lane, [&](int kb, float (&z0)[4], float (&z1)[4]) {
+                        const uint32_t (&o)[4] = fd[kb][0];
+                        const float2 e0 = pair(vec.e + 16 * kb + q0), e1 = pair(vec.e + 16 * kb + 8 + q0);
+                        z0[0] = low(o[0]); z0[1] = high(o[0]); z0[2] = low(o[1]); z0[3] = high(o[1]);
+                        z1[0] = low(o[2]); z1[1] = high(o[2]); z1[2] = low(o[3]); z1[3] = high(o[3]);
+                        scale_cols(z0, make_float2(p.scale * e0.x, p.scale * e0.y));
+                        scale_cols(z1, make_float2(p.scale * e1.x, p.scale * e1.y));
+                    });
 #pragma unroll
                     for (int n = 0; n < D / 8; ++n) zq[n * 32 + lane] = as4(y[n]);
                 }
-                // the state as it is held: [dv, d] in bf16
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint4 s4 = held[ks * 32 + lane];
-                    const uint32_t s2[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const int r = 16 * ks + 8 * (m >> 1) + q0, cc = col + 8 * (m & 1);
-                        if (r < p.d && cc < p.dv)
-                            *reinterpret_cast<uint32_t *>(a.states + (((size_t)bh * a.nc + c) * p.dv + cc) * p.d + r) = s2[m];
-                    }
-                }
+                for (int ks = 0; ks < D / 16; ++ks) was[ks] = held[ks * 32 + lane];
             }
             bar<32 * (KS + 1)>(kBarU + slice);           // U is there; the chain may change `held`
             float z[8][4];
@@ -544,8 +555,12 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             if (MODE == kFwd) {
                 uint32_t fu[4][2][4], o[8][2];
 #pragma unroll
-                for (int kb = 0; kb < 4; ++kb) split_a<2>(z[2 * kb], z[2 * kb + 1], fu[kb]);
-                triangle<false, 2, 1>(x, fu, pt, lane, [](int j) { return j; });
+                for (int kb = 0; kb < 2; ++kb) split_a<2>(z[2 * kb], z[2 * kb + 1], fu[kb]);
+                triangle<false, 2, 1>(x, fu, pt, lane, [](int j) { return j; }, [&](int u) {
+                    const int kb = 2 + u / 2;
+                    split_quarter<2>(z[2 * kb], z[2 * kb + 1], fu[kb], 2 * (u & 1));
+                    split_quarter<2>(z[2 * kb], z[2 * kb + 1], fu[kb], 2 * (u & 1) + 1);
+                });
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
                     o[n][0] = pack(x[n][0], x[n][1]);
@@ -553,6 +568,17 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
                 }
                 to_memory(static_cast<__nv_bfloat16 *>(a.out), c, st, o);
             } else {
+                // the state as it was held: [dv, d] in bf16
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t s2[4] = {was[ks].x, was[ks].y, was[ks].z, was[ks].w};
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const int r = 16 * ks + 8 * (m >> 1) + q0, cc = col + 8 * (m & 1);
+                        if (r < p.d && cc < p.dv)
+                            *reinterpret_cast<uint32_t *>(a.states + (((size_t)bh * a.nc + c) * p.dv + cc) * p.d + r) = s2[m];
+                    }
+                }
                 // W = U / beta (X as it is) in two terms
                 uint32_t t0[8][2], t1[8][2];
 #pragma unroll
@@ -605,20 +631,25 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
         // y = (K S)^T in NT terms of S: this warp's part of the sum over d
         float y[8][4];
         zero(y);
+        uint32_t fs[2][NT][4], fb[2][4][4];
+#pragma unroll
+        for (int np = 0; np < 4; ++np) ldsm(fb[0][np], kt + at<L::kRow>(np * 16 + br, k0 / 8 + bc));
+        split_a<NT>(S[0], S[1], fs[0]);
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
-            uint32_t fs[NT][4];
-            split_a<NT>(S[2 * ks], S[2 * ks + 1], fs);
+            constexpr int kLast = DK / 16 - 1;
+            const int nx = ks < kLast ? ks + 1 : ks;
 #pragma unroll
-            for (int np = 0; np < 4; ++np) {
-                uint32_t fb[4];
-                ldsm(fb, kt + at<L::kRow>(np * 16 + br, k0 / 8 + 2 * ks + bc));
+            for (int t = NT - 1; t >= 0; --t)
 #pragma unroll
-                for (int t = NT - 1; t >= 0; --t) {
-                    mma(y[2 * np], fs[t], fb[0], fb[1]);
-                    mma(y[2 * np + 1], fs[t], fb[2], fb[3]);
+                for (int np = 0; np < 4; ++np) {
+                    mma(y[2 * np], fs[ks & 1][t], fb[ks & 1][np][0], fb[ks & 1][np][1]);
+                    mma(y[2 * np + 1], fs[ks & 1][t], fb[ks & 1][np][2], fb[ks & 1][np][3]);
+                    if (ks < kLast && t == NT - 1) {     // the next step's operands
+                        ldsm(fb[nx & 1][np], kt + at<L::kRow>(np * 16 + br, k0 / 8 + 2 * nx + bc));
+                        split_quarter<NT>(S[2 * nx], S[2 * nx + 1], fs[nx & 1], np);
+                    }
                 }
-            }
         }
         float x[OWN][4];
         if (KS > 1) {
@@ -636,20 +667,18 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             }
             x[j][0] = s4.x; x[j][1] = s4.y; x[j][2] = s4.z; x[j][3] = s4.w;
         }
-        if (BACK) {
-            // dU = f K R + P^T dO
-            bar<32 * (KS + 1)>(kBarZ + slice);
+        // R = beta (V - e^G K S), kBack: dU = f K R + P^T dO, a pair of tiles at a time
+        if (BACK) bar<32 * (KS + 1)>(kBarZ + slice);
+        auto right_side = [&](int j) {
+            if (BACK) {
 #pragma unroll
-            for (int j = 0; j < OWN; ++j) {
-                const float2 f = pair(vec.f + 8 * own(j) + q0);
-                const float4 z = zp[own(j) * 32 + lane];
-                x[j][0] = fmaf(f.x, x[j][0], z.x); x[j][1] = fmaf(f.y, x[j][1], z.y);
-                x[j][2] = fmaf(f.x, x[j][2], z.z); x[j][3] = fmaf(f.y, x[j][3], z.w);
-            }
-        } else {
-            // R = beta (V - e^G K S)
-#pragma unroll
-            for (int j = 0; j < OWN; j += 2) {
+                for (int m = 0; m < 2; ++m) {
+                    const float2 f = pair(vec.f + 8 * own(j + m) + q0);
+                    const float4 z = zp[own(j + m) * 32 + lane];
+                    x[j + m][0] = fmaf(f.x, x[j + m][0], z.x); x[j + m][1] = fmaf(f.y, x[j + m][1], z.y);
+                    x[j + m][2] = fmaf(f.x, x[j + m][2], z.z); x[j + m][3] = fmaf(f.y, x[j + m][3], z.w);
+                }
+            } else {
                 uint32_t fv[4];
                 ldsm_t(fv, vt + at<L::kValRow>((lane >> 4 ? own(j + 1) : own(j)) * 8 + (lane & 7), 2 * slice + bc));
 #pragma unroll
@@ -661,10 +690,14 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
                     x[j + m][3] = be.y * fmaf(-e.y, x[j + m][3], high(fv[2 * m + 1]));
                 }
             }
-        }
+        };
         // U = T R (kBack: X = T^T dU)
         uint32_t fr[4][NT][4];
+        float u[OWN][4];
+        zero(u);
         if (KS > 1) {
+#pragma unroll
+            for (int j = 0; j < OWN; j += 2) right_side(j);
 #pragma unroll
             for (int j = 0; j < OWN; ++j) {
                 uint32_t t0[NT], t1[NT];
@@ -684,14 +717,25 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
                     fr[kb][t][0] = u0.x; fr[kb][t][1] = u0.y; fr[kb][t][2] = u1.x; fr[kb][t][3] = u1.y;
                 }
             meet();
+            triangle<BACK, NT, NT - 1>(u, fr, tt, lane, own, [](int) {});
         } else {
+            // the half of the rows that comes first in the sum, then the other half between its products
+            auto first = [](int kb) { return BACK ? 3 - kb : kb; };
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb) split_a<NT>(x[(2 * kb) % OWN], x[(2 * kb + 1) % OWN], fr[kb]);
+            for (int kb = 0; kb < 2; ++kb) {
+                const int k = first(kb);
+                right_side(2 * k % OWN);
+                split_a<NT>(x[2 * k % OWN], x[(2 * k + 1) % OWN], fr[k]);
+            }
+            triangle<BACK, NT, NT - 1>(u, fr, tt, lane, own, [&](int i) {
+                const int k = first(2 + i / 2);
+                if (i % 2 == 0) right_side(2 * k % OWN);
+                split_quarter<NT>(x[2 * k % OWN], x[(2 * k + 1) % OWN], fr[k], 2 * (i & 1));
+                split_quarter<NT>(x[2 * k % OWN], x[(2 * k + 1) % OWN], fr[k], 2 * (i & 1) + 1);
+            });
         }
-        zero(x);
-        triangle<BACK, NT, NT - 1>(x, fr, tt, lane, own);
 #pragma unroll
-        for (int j = 0; j < OWN; ++j) reinterpret_cast<float4 *>(rows)[own(j) * 32 + lane] = as4(x[j]);
+        for (int j = 0; j < OWN; ++j) reinterpret_cast<float4 *>(rows)[own(j) * 32 + lane] = as4(u[j]);
         bar<32 * (KS + 1)>(kBarU + slice);
         // S <- e^{G_C} S + (f U)^T K  (kBack: R <- e^{G_C} R + the helper's part - (e^G beta X)^T K)
         const float last = vec.last;
@@ -703,23 +747,21 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             S[n][2] = BACK ? fmaf(last, S[n][2], z.z) : last * S[n][2];
             S[n][3] = BACK ? fmaf(last, S[n][3], z.w) : last * S[n][3];
         }
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-            float z[2][4];
+        add_outer<L::kRow, NT>(S, kt, k0 / 8, lane, [&](int kb, float (&z0)[4], float (&z1)[4]) {
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const int n = 2 * kb + m;
-                const float4 u = KS > 1 ? reinterpret_cast<const float4 *>(rows)[n * 32 + lane] : as4(x[n % OWN]);
-                z[m][0] = u.x; z[m][1] = u.y; z[m][2] = u.z; z[m][3] = u.w;
+                const float4 w = KS > 1 ? reinterpret_cast<const float4 *>(rows)[n * 32 + lane] : as4(u[n % OWN]);
+                float (&z)[4] = m ? z1 : z0;
+                z[0] = w.x; z[1] = w.y; z[2] = w.z; z[3] = w.w;
                 float2 f = pair((BACK ? vec.e : vec.f) + 8 * n + q0);
                 if (BACK) {
                     const float2 be = pair(vec.beta + 8 * n + q0);
                     f.x *= -be.x; f.y *= -be.y;
                 }
-                scale_cols(z[m], f);
+                scale_cols(z, f);
             }
-            add_outer<L::kRow, NT>(S, z[0], z[1], kt, kb * 16, k0 / 8, lane);
-        }
+        });
         hold();
         bar<kAll>(kBarAll);
     }
