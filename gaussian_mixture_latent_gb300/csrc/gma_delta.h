@@ -29,6 +29,11 @@ struct DeltaRec {
     float *rows_out;                  // forward: w [G, N, dv]; backward: dU [G, N, dv]; or null
     float *ckpt;                      // [G, ceil(N / kRecChunk), d, dv]: S before / dS after each chunk; or null
 };
+// Rows by kStepRows at a time, from a pool of states (slots); state_in, state_out, slots and out of DeltaRec only.
+// Without state_out at most kStepRows rows.
+constexpr int kStepRows = 8;
+cudaError_t delta_step(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s);
+// Any number of rows; no slots.
 cudaError_t delta_rec_forward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s);
 // p.V is dO; state_in is dL/dS after the last row, state_out dL/dS before the first
 cudaError_t delta_rec_backward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s);

@@ -44,9 +44,8 @@ bool all_aligned(const void *const (&ptrs)[M]) {
 
 gma_status launched(cudaError_t e) { return e == cudaSuccess ? GMA_OK : GMA_ERR_CUDA; }
 
-// Up to this many rows the row-by-row kernel is the faster one: it has no chunk to prepare.
-constexpr int kRecRows = 8;
-bool in_chunks(const DeltaProblem &p) { return delta_tc_supported(p) && p.N > kRecRows; }
+// Up to kStepRows rows the row-by-row kernels are the faster ones: there is no chunk to prepare.
+bool in_chunks(const DeltaProblem &p) { return delta_tc_supported(p) && p.N > kStepRows; }
 
 struct RecLayout {
     size_t w, du, s0, ds, dq, dk, total;
@@ -105,7 +104,8 @@ gma_status gma_delta_forward(const gma_delta_desc *desc, const void *Qx, const v
     r.state_in = state_in;
     r.state_out = state_out;
     r.out = out;
-    return launched(delta_rec_forward(p, r, static_cast<cudaStream_t>(stream)));
+    return launched(p.N > 0 && p.N <= kStepRows ? delta_step(p, r, static_cast<cudaStream_t>(stream))
+                                                : delta_rec_forward(p, r, static_cast<cudaStream_t>(stream)));
 }
 
 gma_status gma_delta_decode_workspace_size(const gma_delta_desc *desc, size_t *bytes) {
@@ -133,7 +133,7 @@ gma_status gma_delta_decode(const gma_delta_desc *desc, const void *Qx, const vo
     r.slots = slots;
     r.n_states = n_states;
     r.out = out;
-    return launched(delta_rec_forward(p, r, static_cast<cudaStream_t>(stream)));
+    return launched(delta_step(p, r, static_cast<cudaStream_t>(stream)));
 }
 
 gma_status gma_delta_backward_workspace_size(const gma_delta_desc *desc, size_t *bytes) {
@@ -205,7 +205,9 @@ static gma_status state_check(const gma_state_desc *d, const float *state, const
     if (store_like && d->n > (d->n_states < d->n_cache ? d->n_states : d->n_cache)) return GMA_ERR_INVALID_ARG;
     const void *const ptrs[] = {state, src, dst, codes, scales, ws};
     if (!all_aligned(ptrs)) return GMA_ERR_INVALID_ARG;
-    if ((long long)d->rows * d->cols > INT_MAX || d->n > 65535) return GMA_ERR_UNSUPPORTED;
+    // 32-bit offsets within a state whose rows are whole groups, and a 32-bit grid (1024 pieces of four or more to a CTA)
+    const long long padded = (long long)d->rows * ((d->cols + 31) / 32) * 32;
+    if (padded > INT_MAX || d->n > 65535 || (padded / 4096 + 1) * d->n > INT_MAX) return GMA_ERR_UNSUPPORTED;
     if (!ws || wsb < kHeaderBytes) return GMA_ERR_WORKSPACE;
     return GMA_OK;
 }

@@ -9,10 +9,13 @@
 //   du_t = R^T k_t + scale (q_t . k_t) dO_t   (R before dO_t's own term is added)
 //   x_t  = beta_t du_t = dV_t,   R <- a_t (R + scale q_t dO_t^T - k_t x_t^T).
 //
-// One CTA of 256 threads holds a [d, VW] slice of the state in registers: a thread has four neighbouring columns of
-// R rows, a warp reads whole row pieces of VW floats, and a row's column sums go over the 8 warps through shared
-// memory (one barrier a row, two buffers).  With one row (decoding) the time is the state's read and write; a long
-// sequence is bound by the latency of the chain (reduce, barrier, update) of each row.
+// Two kernels, by the number of rows.
+// delta_step_kernel (up to kStepRows rows: decoding): one CTA of 256 threads holds a [d, VW] slice of the state in
+// registers; a thread has four neighbouring columns of R rows, a warp reads whole row pieces of VW floats, and a row's
+// column sums go over the 8 warps through shared memory.  The time is the state's read and write.
+// delta_seq_kernel (longer): a warp holds [d, 4] of the state, eight lanes to a column, and needs no other warp: a row's
+// sums are three shuffles.  Four loader warps stage the next 16 rows (and their decays and q.k) meanwhile.  The time is the
+// latency of one row after another.
 #include <cstdint>
 
 #include "gma_delta.h"
@@ -20,67 +23,52 @@
 namespace gma {
 namespace {
 
-constexpr int kThreads = 256, kWarps = 8, kTok = 8;      // kTok: rows staged at a time, one q.k dot to a warp
+constexpr int kThreads = 256, kWarps = 8;
+static_assert(kStepRows <= kWarps, "one row's q.k, and one row's results, to a warp");
 
 struct RecArgs {
     DeltaProblem p;
     DeltaRec r;
-    int slices, tok;
+    int slices;
+    int first, rows;                  // delta_step_kernel: the rows of this launch
 };
 
-template <typename In, int VW, int R, bool BWD>
-__global__ void __launch_bounds__(kThreads) delta_rec_kernel(const RecArgs a) {
+template <typename In, int VW, int R>
+__global__ void __launch_bounds__(kThreads, R <= 8 ? 4 : 2) delta_step_kernel(const RecArgs a) {
     constexpr int kLanes = VW / 4, kRowsWarp = 32 / kLanes;   // lanes of one row piece; row pieces of a warp
     extern __shared__ __align__(16) float sm[];
     const DeltaProblem &p = a.p;
     const int d = p.d, dv = p.dv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int d4 = (d + 3) & ~3;
-    const int pitch = 2 * d4 + VW;
-    float *tok = sm;                                     // [a.tok][q | k | v]
-    float *part = tok + a.tok * pitch;                   // [2][2][kWarps][VW]
-    __shared__ float s_a[kTok], s_beta[kTok], s_qk[kTok];
+    const int d4 = (d + 3) & ~3, pitch = 2 * d4 + VW;
+    float *tok = sm;                                     // [rows][q | k | v]
+    float *part = tok + a.rows * pitch;                  // [2][2][kWarps][VW]
+    __shared__ float s_a[kStepRows], s_beta[kStepRows], s_qk[kStepRows];
     const int slice = blockIdx.x % a.slices;
     const int bh = blockIdx.x / a.slices, b = bh / p.H, h = bh % p.H;
     const int hk = h / (p.H / p.Hk);
     const int c0 = slice * VW + (lane % kLanes) * 4, rsub = lane / kLanes;
-    const int len = delta_len(p.lengths, b, p.N);
+    const int len = min(max(delta_len(p.lengths, b, p.N) - a.first, 0), a.rows);
 
-    int slot = b;
-    bool mine = true;
-    if (a.r.slots) {
-        // a negative slot marks a batch entry that is not there; a slot outside the pool, or one that an earlier
-        // entry already has, is an error: either way the entry touches no state
-        slot = a.r.slots[b];
-        bool twice = false;
-        for (int j = tid; j < b; j += kThreads) twice |= a.r.slots[j] == slot;
-        twice = __syncthreads_or(twice);
-        const bool bad = slot >= a.r.n_states || (slot >= 0 && twice);
-        if (bad && tid == 0) atomicOr(p.status, (unsigned)kDevErrBounds);
-        mine = slot >= 0 && !bad;
-    }
-    const size_t head_rows = (size_t)bh * p.N;
-    const size_t key_rows = ((size_t)b * p.Hk + hk) * p.N;
+    const size_t head_rows = (size_t)bh * p.N + a.first;
+    const size_t key_rows = ((size_t)b * p.Hk + hk) * p.N + a.first;
     In *out = static_cast<In *>(a.r.out);
-    const int live = mine ? len : 0;
-    // rows that do not exist are written as zeros
-    for (size_t i = tid; i < (size_t)(p.N - live) * VW; i += kThreads) {
-        const int c = slice * VW + (int)(i % VW);
-        if (c < dv) delta_out(out, (head_rows + live + i / VW) * dv + c, 0.f);
-    }
-    if (!mine) return;
-
+    // a negative slot marks a batch entry that is not there; a slot outside the pool, or one that an earlier entry
+    // already has, is an error: either way the entry touches no state.  Every read that does not depend on the last of
+    // these checks starts before it.
+    const int slot = a.r.slots ? a.r.slots[b] : b;
+    const bool inside = !a.r.slots || (slot >= 0 && slot < a.r.n_states);
     float S[R][4];
     const bool vec = (dv & 3) == 0;
-    const size_t sbase = ((size_t)slot * p.H + h) * d * dv;
+    const size_t sbase = ((size_t)max(slot, 0) * p.H + h) * d * dv;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int r = (i * kWarps + warp) * kRowsWarp + rsub;
 #pragma unroll
         for (int j = 0; j < 4; ++j) S[i][j] = 0.f;
-        if (a.r.state_in && r < d) {
+        if (inside && a.r.state_in && r < d) {
             const float *src = a.r.state_in + sbase + (size_t)r * dv + c0;
             if (vec) {
-                if (c0 < dv) *reinterpret_cast<float4 *>(S[i]) = *reinterpret_cast<const float4 *>(src);
+                if (c0 < dv) *reinterpret_cast<float4 *>(S[i]) = __ldcs(reinterpret_cast<const float4 *>(src));
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -88,170 +76,297 @@ __global__ void __launch_bounds__(kThreads) delta_rec_kernel(const RecArgs a) {
             }
         }
     }
-    auto write_state = [&](float *dst) {
+    const In *Q = static_cast<const In *>(p.Qx), *K = static_cast<const In *>(p.Kx), *V = static_cast<const In *>(p.V);
+    for (int t = 0; t < len; ++t) {
+        float *row = tok + t * pitch;
+        for (int e = tid; e < pitch; e += kThreads) {
+            float x = 0.f;
+            if (e < d4) {
+                if (e < d) x = delta_in(Q, (key_rows + t) * d + e);
+            } else if (e < 2 * d4) {
+                if (e - d4 < d) x = delta_in(K, (key_rows + t) * d + e - d4);
+            } else {
+                const int c = slice * VW + e - 2 * d4;
+                if (c < dv) x = delta_in(V, (head_rows + t) * dv + c);
+            }
+            row[e] = x;
+        }
+    }
+    if (tid < len) {
+        s_a[tid] = expf(delta_gate(p.g, head_rows + tid, p.gate_bf16));
+        s_beta[tid] = delta_gate(p.beta, head_rows + tid, p.gate_bf16);
+    }
+    bool twice = false;
+    if (a.r.slots)
+        for (int j = tid; j < b; j += kThreads) twice |= a.r.slots[j] == slot;
+    twice = __syncthreads_or(twice);                     // also: the staged rows are there
+    const bool mine = inside && !twice;
+    if (!mine && (slot >= a.r.n_states || (slot >= 0 && twice)) && tid == 0) atomicOr(p.status, (unsigned)kDevErrBounds);
+    // rows that do not exist are written as zeros
+    const int live = mine ? len : 0;
+    for (int i = tid; i < (a.rows - live) * VW; i += kThreads) {
+        const int c = slice * VW + i % VW;
+        if (c < dv) delta_out(out, (head_rows + live + i / VW) * dv + c, 0.f);
+    }
+    if (!mine) return;
+    if (warp < len) {
+        const float *q = tok + warp * pitch, *k = q + d4;
+        float x = 0.f;
+        for (int i = lane; i < d; i += 32) x = fmaf(q[i], k[i], x);
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+        if (lane == 0) s_qk[warp] = x;
+    }
+    const int cl = (lane % kLanes) * 4;
+    for (int t = 0; t < len; ++t) {
+        const float *q = tok + t * pitch, *k = q + d4;
+        float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int r = (i * kWarps + warp) * kRowsWarp + rsub;
-            if (r >= d) continue;
-            float *to = dst + (size_t)r * dv + c0;
-            if (vec) {
-                if (c0 < dv) *reinterpret_cast<float4 *>(to) = *reinterpret_cast<float4 *>(S[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (c0 + j < dv) to[j] = S[i][j];
-            }
-        }
-    };
-    const int nchunk = (p.N + kRecChunk - 1) / kRecChunk;
-    float *ckpt = a.r.ckpt ? a.r.ckpt + (size_t)bh * nchunk * d * dv : nullptr;
-
-    const In *Q = static_cast<const In *>(p.Qx), *K = static_cast<const In *>(p.Kx), *V = static_cast<const In *>(p.V);
-    for (int done = 0; done < len; done += a.tok) {
-        const int nt = min(a.tok, len - done);
-        __syncthreads();                                 // the last block's rows have been read
-        for (int i = tid; i < nt * pitch; i += kThreads) {
-            const int t = i / pitch, e = i % pitch;
-            const int row = BWD ? len - 1 - done - t : done + t;
-            float x = 0.f;
-            if (e < 2 * d4) {
-                const int c = e < d4 ? e : e - d4;
-                if (c < d) x = delta_in(e < d4 ? Q : K, (key_rows + row) * d + c);
-            } else {
-                const int c = slice * VW + e - 2 * d4;
-                if (c < dv) x = delta_in(V, (head_rows + row) * dv + c);
-            }
-            tok[i] = x;
-        }
-        if (tid < nt) {
-            const int row = BWD ? len - 1 - done - tid : done + tid;
-            s_a[tid] = expf(delta_gate(p.g, head_rows + row, p.gate_bf16));
-            s_beta[tid] = delta_gate(p.beta, head_rows + row, p.gate_bf16);
-        }
-        __syncthreads();
-        if (warp < nt) {
-            const float *q = tok + warp * pitch, *k = q + d4;
-            float x = 0.f;
-            for (int i = lane; i < d; i += 32) x = fmaf(q[i], k[i], x);
-            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-            if (lane == 0) s_qk[warp] = x;
-        }
-        for (int t = 0; t < nt; ++t) {
-            const int row = BWD ? len - 1 - done - t : done + t;
-            if (ckpt) {
-                if (!BWD && row % kRecChunk == 0) write_state(ckpt + (size_t)(row / kRecChunk) * d * dv);
-                if (BWD && (row % kRecChunk == kRecChunk - 1 || row == len - 1))
-                    write_state(ckpt + (size_t)(row / kRecChunk) * d * dv);
-            }
-            const float *q = tok + t * pitch, *k = q + d4;
-            float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const int r = (i * kWarps + warp) * kRowsWarp + rsub;
-                const float kr = r < d ? k[r] : 0.f, qr = !BWD && r < d ? q[r] : 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    pk[j] = fmaf(kr, S[i][j], pk[j]);
-                    if (!BWD) pq[j] = fmaf(qr, S[i][j], pq[j]);
-                }
-            }
-#pragma unroll
-            for (int o = 16; o >= kLanes; o >>= 1)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    pk[j] += __shfl_xor_sync(~0u, pk[j], o);
-                    if (!BWD) pq[j] += __shfl_xor_sync(~0u, pq[j], o);
-                }
-            float *pb = part + (t & 1) * 2 * kWarps * VW;
-            const int cl = (lane % kLanes) * 4;
-            if (rsub == 0) {
-                *reinterpret_cast<float4 *>(pb + warp * VW + cl) = make_float4(pk[0], pk[1], pk[2], pk[3]);
-                if (!BWD)
-                    *reinterpret_cast<float4 *>(pb + (kWarps + warp) * VW + cl) = make_float4(pq[0], pq[1], pq[2], pq[3]);
-            }
-            __syncthreads();
-            float ks[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float4 x = *reinterpret_cast<const float4 *>(pb + w * VW + cl);
-                ks[0] += x.x; ks[1] += x.y; ks[2] += x.z; ks[3] += x.w;
-            }
-            const float dec = s_a[t], beta = s_beta[t], qk = s_qk[t];
-            const float4 v4 = *reinterpret_cast<const float4 *>(tok + t * pitch + 2 * d4 + cl);
-            const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-            float y[4], u[4];                            // forward: w, u; backward: du, x
+            const float kr = r < d ? k[r] : 0.f, qr = r < d ? q[r] : 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                y[j] = BWD ? fmaf(p.scale * qk, v[j], ks[j]) : fmaf(-dec, ks[j], v[j]);
-                u[j] = beta * y[j];
-            }
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const int r = (i * kWarps + warp) * kRowsWarp + rsub;
-                const float kr = r < d ? k[r] : 0.f;
-                if (BWD) {
-                    const float qr = r < d ? p.scale * q[r] : 0.f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) S[i][j] = dec * fmaf(-kr, u[j], fmaf(qr, v[j], S[i][j]));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) S[i][j] = fmaf(kr, u[j], dec * S[i][j]);
-                }
-            }
-            if (warp == t && rsub == 0) {                // one warp a row writes the results (kTok <= kWarps)
-                float o[4];
-                if (BWD) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) o[j] = u[j];
-                } else {
-                    float qs[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
-                        const float4 x = *reinterpret_cast<const float4 *>(pb + (kWarps + w) * VW + cl);
-                        qs[0] += x.x; qs[1] += x.y; qs[2] += x.z; qs[3] += x.w;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) o[j] = p.scale * fmaf(dec, qs[j], qk * u[j]);
-                }
-                const size_t at = (head_rows + row) * dv + c0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (c0 + j < dv) {
-                        delta_out(out, at + j, o[j]);
-                        if (a.r.rows_out) a.r.rows_out[at + j] = y[j];
-                    }
+                pk[j] = fmaf(kr, S[i][j], pk[j]);
+                pq[j] = fmaf(qr, S[i][j], pq[j]);
             }
         }
+#pragma unroll
+        for (int o = 16; o >= kLanes; o >>= 1)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                pk[j] += __shfl_xor_sync(~0u, pk[j], o);
+                pq[j] += __shfl_xor_sync(~0u, pq[j], o);
+            }
+        float *pb = part + (t & 1) * 2 * kWarps * VW;
+        if (rsub == 0) {
+            *reinterpret_cast<float4 *>(pb + warp * VW + cl) = make_float4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<float4 *>(pb + (kWarps + warp) * VW + cl) = make_float4(pq[0], pq[1], pq[2], pq[3]);
+        }
+        __syncthreads();
+        float ks[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 x = *reinterpret_cast<const float4 *>(pb + w * VW + cl);
+            ks[0] += x.x; ks[1] += x.y; ks[2] += x.z; ks[3] += x.w;
+        }
+        const float dec = s_a[t], beta = s_beta[t], qk = s_qk[t];
+        const float4 v4 = *reinterpret_cast<const float4 *>(tok + t * pitch + 2 * d4 + cl);
+        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+        float u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = beta * fmaf(-dec, ks[j], v[j]);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = (i * kWarps + warp) * kRowsWarp + rsub;
+            const float kr = r < d ? k[r] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[i][j] = fmaf(dec, S[i][j], kr * u[j]);
+        }
+        if (warp == t && rsub == 0) {                    // one warp a row writes the results (kStepRows <= kWarps)
+            float qs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 x = *reinterpret_cast<const float4 *>(pb + (kWarps + w) * VW + cl);
+                qs[0] += x.x; qs[1] += x.y; qs[2] += x.z; qs[3] += x.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c0 + j < dv)
+                    delta_out(out, (head_rows + t) * dv + c0 + j, p.scale * fmaf(dec, qs[j], qk * u[j]));
+        }
     }
-    if (a.r.state_out) write_state(a.r.state_out + sbase);
+    if (!a.r.state_out) return;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int r = (i * kWarps + warp) * kRowsWarp + rsub;
+        if (r >= d) continue;
+        float *to = a.r.state_out + sbase + (size_t)r * dv + c0;
+        if (vec) {
+            if (c0 < dv) __stcs(reinterpret_cast<float4 *>(to), *reinterpret_cast<float4 *>(S[i]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c0 + j < dv) to[j] = S[i][j];
+        }
+    }
 }
 
-template <typename In, int VW, int R, bool BWD>
-cudaError_t launch_rec(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
-    RecArgs a{p, r, (p.dv + VW - 1) / VW, p.N < kTok ? p.N : kTok};
+template <typename In, int VW, int R>
+cudaError_t launch_step(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
+    RecArgs a{p, r, (p.dv + VW - 1) / VW, 0, 0};
     const int d4 = (p.d + 3) & ~3;
-    const size_t smem = sizeof(float) * ((size_t)a.tok * (2 * d4 + VW) + 4 * kWarps * VW);
-    delta_rec_kernel<In, VW, R, BWD><<<(unsigned)((size_t)p.B * p.H * a.slices), kThreads, smem, s>>>(a);
+    cudaError_t e = cudaSuccess;
+    for (a.first = 0; a.first < p.N && e == cudaSuccess; a.first += kStepRows) {
+        a.rows = p.N - a.first < kStepRows ? p.N - a.first : kStepRows;
+        const size_t smem = sizeof(float) * ((size_t)a.rows * (2 * d4 + VW) + 4 * kWarps * VW);
+        delta_step_kernel<In, VW, R><<<(unsigned)((size_t)p.B * p.H * a.slices), kThreads, smem, s>>>(a);
+        e = cudaGetLastError();
+        a.r.state_in = a.r.state_out;
+    }
+    return e;
+}
+
+template <typename In>
+cudaError_t step_dispatch(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
+    if (p.d <= 64) return launch_step<In, 64, 4>(p, r, s);
+    if (p.d <= 128) return launch_step<In, 64, 8>(p, r, s);
+    return launch_step<In, 64, 16>(p, r, s);
+}
+
+// ----------------------------------------------------------------------------------------------------------------
+constexpr int kSeqWarps = 8, kSeqLoaders = 4, kSeqRows = 16, kSeqCols = 4 * kSeqWarps;
+constexpr int kSeqThreads = 32 * (kSeqWarps + kSeqLoaders);
+
+// R4: float4s of the state's column in a lane; lane (8 row groups, 4 columns) has rows 32 i + 4 (lane / 4) + 0..3.
+template <typename In, int R4, bool BWD>
+__global__ void __launch_bounds__(kSeqThreads) delta_seq_kernel(const RecArgs a) {
+    constexpr int kD = 32 * R4, kPitch = 2 * kD + kSeqCols;
+    extern __shared__ __align__(16) float sm[];          // [2][kSeqRows][q | k | v]
+    __shared__ float4 s_row[2][kSeqRows];                // decay, beta, q.k
+    const DeltaProblem &p = a.p;
+    const int d = p.d, dv = p.dv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int slice = blockIdx.x % a.slices;
+    const int bh = blockIdx.x / a.slices, b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
+    const int len = delta_len(p.lengths, b, p.N), blocks = (len + kSeqRows - 1) / kSeqRows;
+    const size_t head_rows = (size_t)bh * p.N, key_rows = ((size_t)b * p.Hk + hk) * p.N;
+    In *out = static_cast<In *>(a.r.out);
+    auto row_of = [&](int t) { return BWD ? len - 1 - t : t; };
+
+    if (warp >= kSeqWarps) {
+        const In *Q = static_cast<const In *>(p.Qx), *K = static_cast<const In *>(p.Kx), *V = static_cast<const In *>(p.V);
+        const int lw = warp - kSeqWarps, vc = slice * kSeqCols + lane;
+        for (int blk = 0; blk <= blocks; ++blk) {
+            if (blk < blocks) {
+                constexpr int kEach = kSeqRows / kSeqLoaders;
+                float q[kEach][R4], k[kEach][R4], v[kEach], ga[kEach], be[kEach];
+#pragma unroll
+                for (int m = 0; m < kEach; ++m) {        // every read first, then what is done with them
+                    const int t = blk * kSeqRows + m * kSeqLoaders + lw, row = row_of(t);
+                    const bool in = t < len;
+                    v[m] = in && vc < dv ? delta_in(V, (head_rows + row) * dv + vc) : 0.f;
+                    ga[m] = in ? delta_gate(p.g, head_rows + row, p.gate_bf16) : 0.f;
+                    be[m] = in ? delta_gate(p.beta, head_rows + row, p.gate_bf16) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < R4; ++i) {
+                        const int e = 32 * i + lane;
+                        q[m][i] = in && e < d ? delta_in(Q, (key_rows + row) * d + e) : 0.f;
+                        k[m][i] = in && e < d ? delta_in(K, (key_rows + row) * d + e) : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < kEach; ++m) {
+                    const int t = m * kSeqLoaders + lw;
+                    float *to = sm + ((blk & 1) * kSeqRows + t) * kPitch;
+                    float x = 0.f;
+#pragma unroll
+                    for (int i = 0; i < R4; ++i) {
+                        to[32 * i + lane] = q[m][i];
+                        to[kD + 32 * i + lane] = k[m][i];
+                        x = fmaf(q[m][i], k[m][i], x);
+                    }
+                    to[2 * kD + lane] = v[m];
+                    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+                    if (lane == 0) s_row[blk & 1][t] = make_float4(expf(ga[m]), be[m], x, 0.f);
+                }
+            }
+            __syncthreads();
+        }
+        // rows that do not exist are written as zeros
+        const int w = min(kSeqCols, dv - slice * kSeqCols);
+        for (size_t i = tid - 32 * kSeqWarps; i < (size_t)(p.N - len) * w; i += 32 * kSeqLoaders)
+            delta_out(out, (head_rows + len + i / w) * dv + slice * kSeqCols + (int)(i % w), 0.f);
+        return;
+    }
+
+    const int c = slice * kSeqCols + 4 * warp + (lane & 3), lr = lane >> 2;
+    const size_t sbase = (size_t)bh * d * dv;
+    const int nchunk = (p.N + kRecChunk - 1) / kRecChunk;
+    float S[R4][4];
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < R4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 32 * i + 4 * lr + j;
+                if (r < d && c < dv) f(S[i][j], (size_t)r * dv + c);
+            }
+    };
+#pragma unroll
+    for (int i = 0; i < R4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[i][j] = 0.f;
+    if (a.r.state_in) each([&](float &x, size_t at) { x = a.r.state_in[sbase + at]; });
+    float keep_o = 0.f, keep_y = 0.f;                    // the results of row t % 8 = lr
+    __syncthreads();
+    for (int blk = 0; blk < blocks; ++blk) {
+        const int n = min(kSeqRows, len - blk * kSeqRows);
+        const float *base = sm + (blk & 1) * kSeqRows * kPitch;
+#pragma unroll 2
+        for (int t = 0; t < n; ++t) {
+            const int row = row_of(blk * kSeqRows + t);
+            if (a.r.ckpt && (BWD ? row % kRecChunk == kRecChunk - 1 || row == len - 1 : row % kRecChunk == 0)) {
+                float *to = a.r.ckpt + ((size_t)bh * nchunk + row / kRecChunk) * d * dv;
+                each([&](float &x, size_t at) { to[at] = x; });
+            }
+            const float4 *q4 = reinterpret_cast<const float4 *>(base + t * kPitch) + lr, *k4 = q4 + kD / 4;
+            const float4 f = s_row[blk & 1][t];
+            const float v = base[t * kPitch + 2 * kD + 4 * warp + (lane & 3)];
+            float kx[R4][4], qx[R4][4], pk[4] = {}, pq[4] = {};
+#pragma unroll
+            for (int i = 0; i < R4; ++i) {
+                *reinterpret_cast<float4 *>(kx[i]) = k4[8 * i];
+                *reinterpret_cast<float4 *>(qx[i]) = q4[8 * i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    pk[j] = fmaf(kx[i][j], S[i][j], pk[j]);
+                    if (!BWD) pq[j] = fmaf(qx[i][j], S[i][j], pq[j]);
+                }
+            }
+            float ks = (pk[0] + pk[1]) + (pk[2] + pk[3]), qs = (pq[0] + pq[1]) + (pq[2] + pq[3]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                ks += __shfl_xor_sync(~0u, ks, o);
+                if (!BWD) qs += __shfl_xor_sync(~0u, qs, o);
+            }
+            const float y = BWD ? fmaf(p.scale * f.z, v, ks) : fmaf(-f.x, ks, v), u = f.y * y;
+            const float sv = p.scale * v;
+#pragma unroll
+            for (int i = 0; i < R4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    // one rounding at the state's size a row; the row's own part is smaller
+                    S[i][j] = fmaf(f.x, S[i][j], BWD ? f.x * fmaf(qx[i][j], sv, -kx[i][j] * u) : kx[i][j] * u);
+            if (t % 8 == lr) {
+                keep_o = BWD ? u : p.scale * fmaf(f.x, qs, f.z * u);
+                keep_y = y;
+            }
+            if ((t % 8 == 7 || t == n - 1) && lr <= t % 8 && c < dv) {       // eight rows' results at a time
+                const size_t at = (head_rows + row_of(blk * kSeqRows + t / 8 * 8 + lr)) * dv + c;
+                delta_out(out, at, keep_o);
+                if (a.r.rows_out) a.r.rows_out[at] = keep_y;
+            }
+        }
+        __syncthreads();
+    }
+    if (a.r.state_out) each([&](float &x, size_t at) { a.r.state_out[sbase + at] = x; });
+}
+
+template <typename In, int R4, bool BWD>
+cudaError_t launch_seq(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
+    const RecArgs a{p, r, (p.dv + kSeqCols - 1) / kSeqCols, 0, 0};
+    constexpr int smem = 2 * kSeqRows * (64 * R4 + kSeqCols) * (int)sizeof(float);
+    const cudaError_t e = set_dyn_smem((const void *)delta_seq_kernel<In, R4, BWD>, smem);
+    if (e != cudaSuccess) return e;
+    delta_seq_kernel<In, R4, BWD><<<(unsigned)((size_t)p.B * p.H * a.slices), kSeqThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
-// The slice width: for one or a few rows the state's traffic is everything, so a CTA takes whole rows (up to 128
-// columns).  For longer sequences the chain of each row is: narrow slices (32 columns) give four times the CTAs and a
-// quarter of the state to each.
 template <typename In, bool BWD>
-cudaError_t rec_dispatch(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
-    if (p.N > kTok) {
-        if (p.d <= 64) return launch_rec<In, 32, 2, BWD>(p, r, s);
-        if (p.d <= 128) return launch_rec<In, 32, 4, BWD>(p, r, s);
-        return launch_rec<In, 32, 8, BWD>(p, r, s);
-    }
-    if (p.dv <= 64 || p.d > 128) {
-        if (p.d <= 64) return launch_rec<In, 64, 4, BWD>(p, r, s);
-        if (p.d <= 128) return launch_rec<In, 64, 8, BWD>(p, r, s);
-        return launch_rec<In, 64, 16, BWD>(p, r, s);
-    }
-    if (p.d <= 64) return launch_rec<In, 128, 8, BWD>(p, r, s);
-    return launch_rec<In, 128, 16, BWD>(p, r, s);
+cudaError_t seq_dispatch(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
+    if (p.d <= 32) return launch_seq<In, 1, BWD>(p, r, s);
+    if (p.d <= 64) return launch_seq<In, 2, BWD>(p, r, s);
+    if (p.d <= 128) return launch_seq<In, 4, BWD>(p, r, s);
+    return launch_seq<In, 8, BWD>(p, r, s);
 }
 
 // ----------------------------------------------------------------------------------------------------------------
@@ -520,12 +635,16 @@ cudaError_t grads_launch(const DeltaProblem &p, const DeltaGrads &a, cudaStream_
 
 }  // namespace
 
+cudaError_t delta_step(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
+    return p.bf16 ? step_dispatch<__nv_bfloat16>(p, r, s) : step_dispatch<float>(p, r, s);
+}
+
 cudaError_t delta_rec_forward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
-    return p.bf16 ? rec_dispatch<__nv_bfloat16, false>(p, r, s) : rec_dispatch<float, false>(p, r, s);
+    return p.bf16 ? seq_dispatch<__nv_bfloat16, false>(p, r, s) : seq_dispatch<float, false>(p, r, s);
 }
 
 cudaError_t delta_rec_backward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
-    return p.bf16 ? rec_dispatch<__nv_bfloat16, true>(p, r, s) : rec_dispatch<float, true>(p, r, s);
+    return p.bf16 ? seq_dispatch<__nv_bfloat16, true>(p, r, s) : seq_dispatch<float, true>(p, r, s);
 }
 
 cudaError_t delta_rec_grads(const DeltaProblem &p, const DeltaGrads &a, cudaStream_t s) {

@@ -25,7 +25,7 @@ struct CopyArgs {
     signed char *codes;
     float *scales;
     int groups;                       // groups of a row
-    long long pieces, per_cta;        // (row, group, sub) pieces of four elements: of a state, of one CTA
+    int pieces, per_cta;              // (row, group, sub) pieces of four elements: of a state, of one CTA
     int ctas;                         // CTAs of one state
 };
 
@@ -46,7 +46,22 @@ __device__ bool copy_pair(const CopyArgs &a, int n_src, int n_dst, int i, int &s
     return src >= 0 && dst >= 0 && !later;
 }
 
-template <bool VEC>
+// Where piece w lies: its element offset in the state, its group and how many of its four elements exist.  FULL: whole
+// groups only, so that pieces and elements run alike and nothing is divided.
+template <bool FULL>
+__device__ __forceinline__ void locate(const CopyArgs &a, int w, bool in, int &off, int &grp, int &n) {
+    grp = w / kSub;
+    if (FULL) {
+        off = 4 * w;
+        n = in ? 4 : 0;
+    } else {
+        const int row = grp / a.groups, col = (grp - row * a.groups) * kGroup + (w % kSub) * 4;
+        off = row * a.p.cols + col;
+        n = in ? min(max(a.p.cols - col, 0), 4) : 0;
+    }
+}
+
+template <bool VEC, bool FULL>
 __global__ void __launch_bounds__(kThreads) state_store_kernel(const CopyArgs a) {
     int src, dst;
     const int i = blockIdx.x / a.ctas;
@@ -54,22 +69,15 @@ __global__ void __launch_bounds__(kThreads) state_store_kernel(const CopyArgs a)
     const float *from = a.state + (size_t)src * a.p.rows * a.p.cols;
     signed char *codes = a.codes + (size_t)dst * a.p.rows * a.p.cols;
     float *scales = a.scales + (size_t)dst * a.p.rows * a.groups;
-    const long long first = (long long)(blockIdx.x % a.ctas) * a.per_cta;
-    const long long last = min(first + a.per_cta, a.pieces);
-    // `first` and `last` are multiples of kSub: the eight threads of a group are there together
-    for (long long at = first + threadIdx.x; at - threadIdx.x < last; at += (long long)kThreads * kUnroll) {
+    const int first = (blockIdx.x % a.ctas) * a.per_cta, count = min(a.per_cta, a.pieces - first);
+    // `first` and `count` are multiples of kSub: the eight threads of a group are there together
+    for (int at = 0; at < count; at += kThreads * kUnroll) {
         float x[kUnroll][4];
-        long long off[kUnroll], grp[kUnroll];
-        int n[kUnroll];
+        int off[kUnroll], grp[kUnroll], n[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const long long w = at + (long long)u * kThreads;
-            const bool in = w < last;
-            grp[u] = in ? w / kSub : 0;
-            const long long row = grp[u] / a.groups;
-            const int col = (int)(grp[u] % a.groups) * kGroup + (int)(w % kSub) * 4;
-            n[u] = in ? min(max(a.p.cols - col, 0), 4) : 0;
-            off[u] = row * a.p.cols + col;
+            const int w = at + u * kThreads + threadIdx.x;
+            locate<FULL>(a, first + w, w < count, off[u], grp[u], n[u]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[u][j] = 0.f;
             if (VEC) {
@@ -82,7 +90,6 @@ __global__ void __launch_bounds__(kThreads) state_store_kernel(const CopyArgs a)
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const bool in = at + (long long)u * kThreads < last;
             float m = 0.f;
             bool odd = false;                            // a NaN or an infinity in the group
 #pragma unroll
@@ -111,12 +118,12 @@ __global__ void __launch_bounds__(kThreads) state_store_kernel(const CopyArgs a)
                 for (int j = 0; j < 4; ++j)
                     if (j < n[u]) codes[off[u] + j] = q[j];
             }
-            if (in && threadIdx.x % kSub == 0) scales[grp[u]] = odd ? __int_as_float(0x7fffffff) : scale;
+            if (n[u] && threadIdx.x % kSub == 0) scales[grp[u]] = odd ? __int_as_float(0x7fffffff) : scale;
         }
     }
 }
 
-template <bool VEC>
+template <bool VEC, bool FULL>
 __global__ void __launch_bounds__(kThreads) state_load_kernel(const CopyArgs a) {
     int src, dst;
     const int i = blockIdx.x / a.ctas;
@@ -124,20 +131,16 @@ __global__ void __launch_bounds__(kThreads) state_load_kernel(const CopyArgs a) 
     const signed char *codes = a.codes + (size_t)src * a.p.rows * a.p.cols;
     const float *scales = a.scales + (size_t)src * a.p.rows * a.groups;
     float *to = a.state + (size_t)dst * a.p.rows * a.p.cols;
-    const long long first = (long long)(blockIdx.x % a.ctas) * a.per_cta;
-    const long long last = min(first + a.per_cta, a.pieces);
-    for (long long at = first + threadIdx.x; at < last; at += (long long)kThreads * kUnroll) {
+    const int first = (blockIdx.x % a.ctas) * a.per_cta, count = min(a.per_cta, a.pieces - first);
+    for (int at = 0; at < count; at += kThreads * kUnroll) {
         char4 q[kUnroll];
         float scale[kUnroll];
-        long long off[kUnroll];
-        int n[kUnroll];
+        int off[kUnroll], n[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const long long w = at + (long long)u * kThreads;
-            const long long grp = w < last ? w / kSub : 0, row = grp / a.groups;
-            const int col = (int)(grp % a.groups) * kGroup + (int)(w % kSub) * 4;
-            n[u] = w < last ? min(max(a.p.cols - col, 0), 4) : 0;
-            off[u] = row * a.p.cols + col;
+            const int w = at + u * kThreads + threadIdx.x;
+            int grp;
+            locate<FULL>(a, first + w, w < count, off[u], grp, n[u]);
             q[u] = make_char4(0, 0, 0, 0);
             if (VEC) {
                 if (n[u]) q[u] = *reinterpret_cast<const char4 *>(codes + off[u]);
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) state_load_kernel(const CopyArgs a) 
         for (int u = 0; u < kUnroll; ++u) {
             const float4 x = make_float4(q[u].x * scale[u], q[u].y * scale[u], q[u].z * scale[u], q[u].w * scale[u]);
             if (VEC) {
-                if (n[u]) *reinterpret_cast<float4 *>(to + off[u]) = x;
+                if (n[u]) __stcs(reinterpret_cast<float4 *>(to + off[u]), x);
             } else {
                 if (n[u] > 0) to[off[u]] = x.x;
                 if (n[u] > 1) to[off[u] + 1] = x.y;
@@ -166,13 +169,11 @@ __global__ void __launch_bounds__(kThreads) state_load_kernel(const CopyArgs a) 
 
 CopyArgs copy_args(const StateCopy &p, float *state, signed char *codes, float *scales) {
     CopyArgs a{p, state, codes, scales, (p.cols + kGroup - 1) / kGroup, 0, 0, 0};
-    a.pieces = p.rows * a.groups * kSub;
-    // eight rounds of the unrolled loop to a CTA; fewer where that would leave most of the GPU idle
-    long long rounds = 8;
-    while (rounds > 1 && (long long)p.n * ((a.pieces + rounds * kThreads * kUnroll - 1) / (rounds * kThreads * kUnroll)) < 608)
-        rounds /= 2;
-    a.per_cta = rounds * kThreads * kUnroll;
-    a.ctas = (int)((a.pieces + a.per_cta - 1) / a.per_cta);
+    a.pieces = (int)(p.rows * a.groups * kSub);
+    // two rounds of the unrolled loop to a CTA; one where that would leave part of the GPU idle
+    const int round = kThreads * kUnroll;
+    a.per_cta = (long long)p.n * ((a.pieces + 2 * round - 1) / (2 * round)) < 1216 ? round : 2 * round;
+    a.ctas = (a.pieces + a.per_cta - 1) / a.per_cta;
     return a;
 }
 
@@ -181,8 +182,9 @@ CopyArgs copy_args(const StateCopy &p, float *state, signed char *codes, float *
 cudaError_t state_store(const StateCopy &p, const float *state, signed char *codes, float *scales, cudaStream_t s) {
     const CopyArgs a = copy_args(p, const_cast<float *>(state), codes, scales);
     const unsigned grid = (unsigned)((long long)a.ctas * p.n);
-    if (p.cols % 4 == 0) state_store_kernel<true><<<grid, kThreads, 0, s>>>(a);
-    else state_store_kernel<false><<<grid, kThreads, 0, s>>>(a);
+    if (p.cols % kGroup == 0) state_store_kernel<true, true><<<grid, kThreads, 0, s>>>(a);
+    else if (p.cols % 4 == 0) state_store_kernel<true, false><<<grid, kThreads, 0, s>>>(a);
+    else state_store_kernel<false, false><<<grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -190,8 +192,9 @@ cudaError_t state_load(const StateCopy &p, const signed char *codes, const float
                        cudaStream_t s) {
     const CopyArgs a = copy_args(p, state, const_cast<signed char *>(codes), const_cast<float *>(scales));
     const unsigned grid = (unsigned)((long long)a.ctas * p.n);
-    if (p.cols % 4 == 0) state_load_kernel<true><<<grid, kThreads, 0, s>>>(a);
-    else state_load_kernel<false><<<grid, kThreads, 0, s>>>(a);
+    if (p.cols % kGroup == 0) state_load_kernel<true, true><<<grid, kThreads, 0, s>>>(a);
+    else if (p.cols % 4 == 0) state_load_kernel<true, false><<<grid, kThreads, 0, s>>>(a);
+    else state_load_kernel<false, false><<<grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -411,7 +411,8 @@ gma_status gma_delta_decode(const gma_delta_desc *desc, const void *Qx, const vo
  *   src, dst [n] int32 or NULL (entry i at i): where each state is read and
  *   written.  A negative index marks an absent entry; an index outside its pool
  *   is skipped and posts GMA_ERR_BOUNDS; of several entries with one
- *   destination the last counts.  n up to 65535, rows * cols below 2^31.
+ *   destination the last counts.  n up to 65535; rows * 32 ceil(cols / 32)
+ *   below 2^31, and that times n / 4096 too (GMA_ERR_UNSUPPORTED beyond).
  * The workspace holds only the status word (256 bytes, zero at first).
  */
 typedef struct {
