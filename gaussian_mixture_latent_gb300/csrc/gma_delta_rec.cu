@@ -33,13 +33,15 @@ struct RecArgs {
     int first, rows;                  // delta_step_kernel: the rows of this launch
 };
 
-template <typename In, int VW, int R>
-__global__ void __launch_bounds__(kThreads, R <= 8 ? 4 : 2) delta_step_kernel(const RecArgs a) {
+// FULL: the slices cover the state exactly, so that no element needs a check.
+template <typename In, int VW, int R, bool FULL>
+__global__ void __launch_bounds__(kThreads, R <= 8 ? 3 : 2) delta_step_kernel(const RecArgs a) {
     constexpr int kLanes = VW / 4, kRowsWarp = 32 / kLanes;   // lanes of one row piece; row pieces of a warp
     extern __shared__ __align__(16) float sm[];
     const DeltaProblem &p = a.p;
-    const int d = p.d, dv = p.dv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int d4 = (d + 3) & ~3, pitch = 2 * d4 + VW;
+    constexpr int kRows = kWarps * kRowsWarp * R;
+    const int d = FULL ? kRows : p.d, dv = p.dv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int d4 = kRows, pitch = 2 * d4 + VW;       // rows past d are zeros
     float *tok = sm;                                     // [rows][q | k | v]
     float *part = tok + a.rows * pitch;                  // [2][2][kWarps][VW]
     __shared__ float s_a[kStepRows], s_beta[kStepRows], s_qk[kStepRows];
@@ -47,6 +49,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 4 : 2) delta_step_kernel(co
     const int bh = blockIdx.x / a.slices, b = bh / p.H, h = bh % p.H;
     const int hk = h / (p.H / p.Hk);
     const int c0 = slice * VW + (lane % kLanes) * 4, rsub = lane / kLanes;
+    const int row0 = (warp * kRowsWarp + rsub) * R;      // the thread's rows: R neighbours, so that k and q are read in fours
     const int len = min(max(delta_len(p.lengths, b, p.N) - a.first, 0), a.rows);
 
     const size_t head_rows = (size_t)bh * p.N + a.first;
@@ -58,17 +61,17 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 4 : 2) delta_step_kernel(co
     const int slot = a.r.slots ? a.r.slots[b] : b;
     const bool inside = !a.r.slots || (slot >= 0 && slot < a.r.n_states);
     float S[R][4];
-    const bool vec = (dv & 3) == 0;
+    const bool vec = FULL || (dv & 3) == 0;
     const size_t sbase = ((size_t)max(slot, 0) * p.H + h) * d * dv;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int r = (i * kWarps + warp) * kRowsWarp + rsub;
+        const int r = row0 + i;
 #pragma unroll
         for (int j = 0; j < 4; ++j) S[i][j] = 0.f;
-        if (inside && a.r.state_in && r < d) {
+        if (inside && a.r.state_in && (FULL || r < d)) {
             const float *src = a.r.state_in + sbase + (size_t)r * dv + c0;
             if (vec) {
-                if (c0 < dv) *reinterpret_cast<float4 *>(S[i]) = __ldcs(reinterpret_cast<const float4 *>(src));
+                if (FULL || c0 < dv) *reinterpret_cast<float4 *>(S[i]) = __ldcs(reinterpret_cast<const float4 *>(src));
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -121,14 +124,17 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 4 : 2) delta_step_kernel(co
         const float *q = tok + t * pitch, *k = q + d4;
         float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int r = (i * kWarps + warp) * kRowsWarp + rsub;
-            const float kr = r < d ? k[r] : 0.f, qr = r < d ? q[r] : 0.f;
+        for (int i = 0; i < R; i += 4) {
+            float kr[4], qr[4];
+            *reinterpret_cast<float4 *>(kr) = *reinterpret_cast<const float4 *>(k + row0 + i);
+            *reinterpret_cast<float4 *>(qr) = *reinterpret_cast<const float4 *>(q + row0 + i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                pk[j] = fmaf(kr, S[i][j], pk[j]);
-                pq[j] = fmaf(qr, S[i][j], pq[j]);
-            }
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    pk[j] = fmaf(kr[m], S[i + m][j], pk[j]);
+                    pq[j] = fmaf(qr[m], S[i + m][j], pq[j]);
+                }
         }
 #pragma unroll
         for (int o = 16; o >= kLanes; o >>= 1)
@@ -156,11 +162,13 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 4 : 2) delta_step_kernel(co
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[j] = beta * fmaf(-dec, ks[j], v[j]);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int r = (i * kWarps + warp) * kRowsWarp + rsub;
-            const float kr = r < d ? k[r] : 0.f;
+        for (int i = 0; i < R; i += 4) {
+            float kr[4];
+            *reinterpret_cast<float4 *>(kr) = *reinterpret_cast<const float4 *>(k + row0 + i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) S[i][j] = fmaf(dec, S[i][j], kr * u[j]);
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[i + m][j] = fmaf(dec, S[i + m][j], kr[m] * u[j]);
         }
         if (warp == t && rsub == 0) {                    // one warp a row writes the results (kStepRows <= kWarps)
             float qs[4] = {0.f, 0.f, 0.f, 0.f};
@@ -171,18 +179,18 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 4 : 2) delta_step_kernel(co
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (c0 + j < dv)
+                if (FULL || c0 + j < dv)
                     delta_out(out, (head_rows + t) * dv + c0 + j, p.scale * fmaf(dec, qs[j], qk * u[j]));
         }
     }
     if (!a.r.state_out) return;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int r = (i * kWarps + warp) * kRowsWarp + rsub;
-        if (r >= d) continue;
+        const int r = row0 + i;
+        if (!FULL && r >= d) continue;
         float *to = a.r.state_out + sbase + (size_t)r * dv + c0;
         if (vec) {
-            if (c0 < dv) __stcs(reinterpret_cast<float4 *>(to), *reinterpret_cast<float4 *>(S[i]));
+            if (FULL || c0 < dv) __stcs(reinterpret_cast<float4 *>(to), *reinterpret_cast<float4 *>(S[i]));
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -193,13 +201,15 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 4 : 2) delta_step_kernel(co
 
 template <typename In, int VW, int R>
 cudaError_t launch_step(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
+    constexpr int kRows = kWarps * (128 / VW) * R;
     RecArgs a{p, r, (p.dv + VW - 1) / VW, 0, 0};
-    const int d4 = (p.d + 3) & ~3;
+    const unsigned grid = (unsigned)((size_t)p.B * p.H * a.slices);
     cudaError_t e = cudaSuccess;
     for (a.first = 0; a.first < p.N && e == cudaSuccess; a.first += kStepRows) {
         a.rows = p.N - a.first < kStepRows ? p.N - a.first : kStepRows;
-        const size_t smem = sizeof(float) * ((size_t)a.rows * (2 * d4 + VW) + 4 * kWarps * VW);
-        delta_step_kernel<In, VW, R><<<(unsigned)((size_t)p.B * p.H * a.slices), kThreads, smem, s>>>(a);
+        const size_t smem = sizeof(float) * ((size_t)a.rows * (2 * kRows + VW) + 4 * kWarps * VW);
+        if (p.d == kRows && p.dv % VW == 0) delta_step_kernel<In, VW, R, true><<<grid, kThreads, smem, s>>>(a);
+        else delta_step_kernel<In, VW, R, false><<<grid, kThreads, smem, s>>>(a);
         e = cudaGetLastError();
         a.r.state_in = a.r.state_out;
     }
@@ -208,6 +218,10 @@ cudaError_t launch_step(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s
 
 template <typename In>
 cudaError_t step_dispatch(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
+    if (p.dv > 64 && p.d <= 128) {
+        if (p.d <= 64) return launch_step<In, 128, 8>(p, r, s);
+        return launch_step<In, 128, 16>(p, r, s);
+    }
     if (p.d <= 64) return launch_step<In, 64, 4>(p, r, s);
     if (p.d <= 128) return launch_step<In, 64, 8>(p, r, s);
     return launch_step<In, 64, 16>(p, r, s);
