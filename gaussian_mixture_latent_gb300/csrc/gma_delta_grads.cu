@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
             for (int i = tid - 256; i < C * 8; i += 128) {           // dV = beta X
                 const int r = i / 8, cc = v0 + i % 8 * 8;
                 if (r >= n_all || cc >= p.dv) continue;
-                const float be = r < n ? delta_gate(p.beta, vrow + r, p.gate_bf16) : 0.f;
+                float be = vec.beta[r];
+                if (fabsf(be) <= 0x1p-64f) be = r < n ? delta_gate(p.beta, vrow + r, p.gate_bf16) : 0.f;     // it was held
                 const uint4 x = *reinterpret_cast<const uint4 *>(sm + L::oX + at<128>(r, i % 8));
                 const uint4 y = *reinterpret_cast<const uint4 *>(sm + L::oX + L::kSlab + at<128>(r, i % 8));
                 auto both = [&](uint32_t h, uint32_t l) { return pack(be * (low(h) + low(l)), be * (high(h) + high(l))); };
@@ -211,7 +212,9 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
     if (role < 2) {
         // E's decays, factors and masks; M = E o (Q or K) K^T: row sums and column sums; E's terms to shared memory
         const float2 g0 = vec.G[i0], g1 = vec.G[i1];
+        const float2 gr = vec.G[rb * 16];
         const float m0 = role ? vec.beta[i0] : p.scale, m1 = role ? vec.beta[i1] : p.scale;
+        const float a0 = m0 * ex2((g0.x - gr.x) + (g0.y - gr.y)), a1 = m1 * ex2((g1.x - gr.x) + (g1.y - gr.y));
         float *col = (role ? col2 : col1) + 64 * rb;
         char *to = sm + L::oE + 2 * role * kTriBytes;
         const uint32_t left = sb + (role == 0 ? L::oQ : 0);
@@ -235,9 +238,13 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
                 if (np <= rb) {
                     const float4 gj = *reinterpret_cast<const float4 *>(vec.G + j);
                     const float2 bj = *reinterpret_cast<const float2 *>(vec.beta + j);
-                    float dd[4] = {ex2((g0.x - gj.x) + (g0.y - gj.y)) * (m0 * bj.x), ex2((g0.x - gj.z) + (g0.y - gj.w)) * (m0 * bj.y),
-                                   ex2((g1.x - gj.x) + (g1.y - gj.y)) * (m1 * bj.x), ex2((g1.x - gj.z) + (g1.y - gj.w)) * (m1 * bj.y)};
-                    if (np == rb) {
+                    if (np < rb) {
+                        // the decay by way of the row block's first row: both factors' exponents are <= 0
+                        const float bx = bj.x * ex2((gr.x - gj.x) + (gr.y - gj.y)), by = bj.y * ex2((gr.x - gj.z) + (gr.y - gj.w));
+                        e[t][0] *= a0 * bx; e[t][1] *= a0 * by; e[t][2] *= a1 * bx; e[t][3] *= a1 * by;
+                    } else {
+                        const float dd[4] = {ex2((g0.x - gj.x) + (g0.y - gj.y)) * (m0 * bj.x), ex2((g0.x - gj.z) + (g0.y - gj.w)) * (m0 * bj.y),
+                                             ex2((g1.x - gj.x) + (g1.y - gj.y)) * (m1 * bj.x), ex2((g1.x - gj.z) + (g1.y - gj.w)) * (m1 * bj.y)};
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             const int i = m < 2 ? i0 : i1, jj = j + (m & 1);
@@ -245,9 +252,6 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
                             // a select and not a product with 0: what lies outside the triangle may be infinite
                             e[t][m] = (role ? jj >= i : jj > i) ? 0.f : e[t][m] * dd[m];
                         }
-                    } else {
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) e[t][m] *= dd[m];
                     }
                     const float s0 = e[t][0] * qk[u][0], s1 = e[t][1] * qk[u][1], s2 = e[t][2] * qk[u][2], s3 = e[t][3] * qk[u][3];
                     d0 += s0 + s1;
@@ -337,12 +341,24 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
         add_e(1, true, sb);
     }
     float *half = reinterpret_cast<float *>(sm + L::oDo);            // the slabs are done with
-    if (role == 0) {
+    // rows i0 and i1 of dQ or dK
+    auto store_rows = [&](__nv_bfloat16 *out, float *heads) {
+        const size_t o0 = (vrow + i0) * p.d + q0, o1 = o0 + (size_t)8 * p.d;
+        const bool in0 = i0 < n_all, in1 = i1 < n_all;
 #pragma unroll
         for (int t = 0; t < D / 8; ++t) {
-            store2(dQ, a.g.dq_heads, i0, 8 * t + q0, acc[t][0], acc[t][1]);
-            store2(dQ, a.g.dq_heads, i1, 8 * t + q0, acc[t][2], acc[t][3]);
+            if (8 * t + q0 >= p.d) continue;
+            if (heads) {
+                if (in0) *reinterpret_cast<float2 *>(heads + o0 + 8 * t) = make_float2(acc[t][0], acc[t][1]);
+                if (in1) *reinterpret_cast<float2 *>(heads + o1 + 8 * t) = make_float2(acc[t][2], acc[t][3]);
+            } else {
+                if (in0) *reinterpret_cast<uint32_t *>(out + o0 + 8 * t) = pack(acc[t][0], acc[t][1]);
+                if (in1) *reinterpret_cast<uint32_t *>(out + o1 + 8 * t) = pack(acc[t][2], acc[t][3]);
+            }
         }
+    };
+    if (role == 0) {
+        store_rows(dQ, a.g.dq_heads);
     } else if (role == 2) {
 #pragma unroll
         for (int t = 0; t < D / 8; ++t) {
@@ -356,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
         for (int t = 0; t < D / 8; ++t) {
             const float2 x = *reinterpret_cast<const float2 *>(half + i0 * L::kPitch + 8 * t + q0);
             const float2 y = *reinterpret_cast<const float2 *>(half + i1 * L::kPitch + 8 * t + q0);
-            store2(dK, a.g.dk_heads, i0, 8 * t + q0, x.x + acc[t][0], x.y + acc[t][1]);
-            store2(dK, a.g.dk_heads, i1, 8 * t + q0, y.x + acc[t][2], y.y + acc[t][3]);
+            acc[t][0] += x.x; acc[t][1] += x.y; acc[t][2] += y.x; acc[t][3] += y.y;
         }
+        store_rows(dK, a.g.dk_heads);
     }
     if (warp == 0) {
         // a: rows and columns of both matrices; running sums from the end of a, from the start of b (two rows to a lane)

@@ -2,9 +2,9 @@
 //
 // A state is a matrix of `rows` rows (all heads) of `cols` fp32 values.  Each row is cut into groups of 32 from its
 // start (the last may be shorter), and a group keeps one fp32 scale:
-//   scale = max |x| / 127,   code = rint(x / scale) in [-127, 127],   read back as code * scale.
-// Both divisions are IEEE fp32 divisions: the format says which code a value on a border gets.  The error of a value
-// is at most half a step, max |x| / 254.  Rounding to 8 bits is the purpose of the cache; the recurrences themselves
+//   scale = max |x| (1 / 127),   code = rint(x / scale) in [-127, 127],   read back as code * scale,
+// in fp32: the product with the rounded 1 / 127, and an IEEE division, so that the format says which code a value on a
+// border gets.  The error of a value is at most half a step, max |x| / 254, and three roundings.  Rounding to 8 bits is the purpose of the cache; the recurrences themselves
 // keep their states in fp32.  In a [K, dv + 1] mixture memory whose dv is a multiple of 32 the normaliser column is a
 // group of its own and comes back to within one rounding.
 //
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) state_store_kernel(const CopyArgs a)
                 m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
                 odd |= __shfl_xor_sync(~0u, (int)odd, o) != 0;
             }
-            const float scale = __fdiv_rn(m, 127.f);
+            const float scale = __fmul_rn(m, 1.f / 127.f);
             signed char q[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

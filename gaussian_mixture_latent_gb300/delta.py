@@ -54,69 +54,86 @@ _FLOATS = (torch.float32, torch.bfloat16)
 _scratch: dict = {}
 
 
-def _check(t, name, shape, dtypes, device):
-    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.is_contiguous()
-            and t.device == device and t.is_cuda):
+_raw_stream = torch._C._cuda_getCurrentRawStream       # the current stream's handle without a Stream object
+
+
+def _check(t, name, shape, dtypes, index):
+    """t is a contiguous CUDA tensor of this shape and of one of these types on device `index`."""
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.get_device() == index
+            and t.is_contiguous()):
         return
     _gma._check(t, name, shape, dtypes)
-    raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
 class _Call:
     """The device, stream and workspace of one call."""
 
-    def __init__(self, what, device, stream, workspace):
-        if device.type != "cuda":
+    __slots__ = ("what", "index", "workspace", "stream", "ptr", "here")
+
+    def __init__(self, what, tensor, stream, workspace):
+        if not tensor.is_cuda:
             raise ValueError(f"{what}: tensors must be CUDA tensors")
-        self.what, self.device, self.workspace = what, device, workspace
-        self.here = torch.cuda.current_device() == device.index
-        current = torch.cuda.current_stream(device)
-        self.stream = current if stream is None else stream
-        self.ptr = self.stream.cuda_stream
+        self.what, self.index, self.workspace, self.stream = what, tensor.get_device(), workspace, stream
+        self.ptr = _raw_stream(self.index)
+        self.here = torch.cuda.current_device() == self.index
         if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
-            self.here = self.here and self.ptr == current.cuda_stream
+            if stream.device.index != self.index:
+                raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {tensor.device}")
+            self.here = self.here and self.ptr == stream.cuda_stream
+            self.ptr = stream.cuda_stream
+
+    def _there(self):
+        """The device and stream made current, for a call from elsewhere."""
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.index)
+        return torch.cuda.device(self.index), torch.cuda.stream(s)
 
     def empty(self, shape, dtype):
         """New memory on the call's device and stream."""
         if self.here:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.device(self.device), torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(shape, dtype=dtype, device=_device(self.index))
+        device, stream = self._there()
+        with device, stream:
+            return torch.empty(shape, dtype=dtype, device=_device(self.index))
 
     def run(self, fn, need, args, check_status):
         if self.here:
             return self._run(fn, need, args, check_status)
-        with torch.cuda.device(self.device), torch.cuda.stream(self.stream):
+        device, stream = self._there()
+        with device, stream:
             self._run(fn, need, args, check_status)
 
     def _run(self, fn, need, args, check_status):
-        ws = self._workspace(need)
+        ws = self.workspace
+        if ws is None:
+            # a buffer of this device and stream; a graph that is being captured gets one of its own
+            capturing = torch.cuda.is_current_stream_capturing()
+            ws = None if capturing else _scratch.get((self.index, self.ptr))
+            if ws is None or ws.numel() < need:
+                # allocated on the call's own stream, so that a buffer that is replaced is reused in its order
+                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=_device(self.index))
+                _gma.gma_workspace_init(ws)
+                if not capturing:
+                    _scratch[(self.index, self.ptr)] = ws
+        elif (ws.get_device() != self.index or ws.dtype != torch.uint8 or not ws.is_contiguous()):
+            raise ValueError(f"{self.what}: workspace must be a contiguous uint8 tensor on cuda:{self.index}")
+        elif ws.numel() < need:
+            raise _gma.GmaError(3, self.what)
         rc = fn(*args, ws.data_ptr(), ws.numel(), self.ptr)
         if rc:
             raise _gma.GmaError(rc, self.what)
         if check_status:
             _gma._check_device_status(ws, self.stream, self.what)
 
-    def _workspace(self, need):
-        ws = self.workspace
-        if ws is not None:
-            if not ws.is_cuda or ws.device != self.device or ws.dtype != torch.uint8 or not ws.is_contiguous():
-                raise ValueError(f"{self.what}: workspace must be a contiguous uint8 tensor on {self.device}")
-            if ws.numel() < need:
-                raise _gma.GmaError(3, self.what)
-            return ws
-        key = (self.device.index, self.ptr)
-        capturing = torch.cuda.is_current_stream_capturing()
-        ws = None if capturing else _scratch.get(key)
-        if ws is None or ws.numel() < need:
-            # allocated on the call's own stream, so that a buffer that is replaced is reused in its order
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
-            _gma.gma_workspace_init(ws, self.stream)
-            if not capturing:
-                _scratch[key] = ws
-        return ws
+
+_devices: dict = {}
+
+
+def _device(index):
+    d = _devices.get(index)
+    if d is None:
+        d = _devices[index] = torch.device("cuda", index)
+    return d
 
 
 def _ptr(t):
@@ -134,9 +151,10 @@ def _sequence(what, size, Qx, Kx, V, g, beta, lengths, scale, stream, workspace)
         if t.dim() != dims:
             raise ValueError(f"{name} has {t.dim()} dimensions, expected {dims}")
     B, Hk, N, d = keys = Qx.shape
-    H, dv = V.shape[1], V.shape[3]
-    dev, dt, gt = Qx.device, Qx.dtype, g.dtype
-    call = _Call(what, dev, stream, workspace)
+    _, H, _, dv = V.shape
+    dt, gt = Qx.dtype, g.dtype
+    call = _Call(what, Qx, stream, workspace)
+    dev = call.index
     _check(Qx, "Qx", keys, _FLOATS, dev)
     _check(Kx, "Kx", keys, (dt,), dev)
     _check(V, "V", (B, H, N, dv), (dt,), dev)
@@ -176,11 +194,11 @@ def gma_delta_forward(Qx, Kx, V, g, beta, state=None, lengths=None, scale=None, 
     if out is None:
         out = call.empty(V.shape, V.dtype)
     else:
-        _check(out, "out", V.shape, (V.dtype,), call.device)
+        _check(out, "out", V.shape, (V.dtype,), call.index)
     if state is not None:
-        _check(state, "state", shape, (torch.float32,), call.device)
+        _check(state, "state", shape, (torch.float32,), call.index)
     if state_out is not None:
-        _check(state_out, "state_out", shape, (torch.float32,), call.device)
+        _check(state_out, "state_out", shape, (torch.float32,), call.index)
     elif return_state:
         state_out = call.empty(shape, torch.float32)
     call.run(_lib().gma_delta_forward, need,
@@ -197,18 +215,18 @@ def gma_delta_backward(Qx, Kx, V, g, beta, dO, state=None, dstate=None, lengths=
     `grads`, if given, is that tuple of preallocated outputs (overwritten)."""
     desc, need, call = _sequence("gma_delta_backward", "gma_delta_backward_workspace_size", Qx, Kx, V, g, beta, lengths,
                                  scale, stream, workspace)
-    _check(dO, "dO", V.shape, (V.dtype,), call.device)
+    _check(dO, "dO", V.shape, (V.dtype,), call.index)
     shape = (desc.B, desc.H, desc.d, desc.dv)
     for name, t in (("state", state), ("dstate", dstate)):
         if t is not None:
-            _check(t, name, shape, (torch.float32,), call.device)
+            _check(t, name, shape, (torch.float32,), call.index)
     inputs = (Qx, Kx, V, g, beta, state)
     if grads is None:
         grads = tuple(None if t is None else call.empty(t.shape, t.dtype) for t in inputs)
     else:
         for t, like, name in zip(grads, inputs, ("dQx", "dKx", "dV", "dg", "dbeta", "dstate_in")):
             if like is not None:
-                _check(t, name, like.shape, (like.dtype,), call.device)
+                _check(t, name, like.shape, (like.dtype,), call.index)
     dstate_in = grads[5] if state is not None else None
     call.run(_lib().gma_delta_backward, need,
              (ctypes.byref(desc),) + tuple(_ptr(t) for t in (Qx, Kx, V, g, beta, lengths, state, dO, dstate) +
@@ -230,13 +248,13 @@ def gma_delta_decode(Qx, Kx, V, g, beta, state, slots=None, lengths=None, scale=
     if state.dim() != 4:
         raise ValueError(f"state has {state.dim()} dimensions, expected 4")
     pool = state.shape[0]
-    _check(state, "state", (pool, V.shape[1], Qx.shape[3], V.shape[3]), (torch.float32,), call.device)
+    _check(state, "state", (pool, V.shape[1], Qx.shape[3], V.shape[3]), (torch.float32,), call.index)
     if slots is not None:
-        _check(slots, "slots", (V.shape[0],), (torch.int32,), call.device)
+        _check(slots, "slots", (V.shape[0],), (torch.int32,), call.index)
     if out is None:
         out = call.empty(V.shape, V.dtype)
     else:
-        _check(out, "out", V.shape, (V.dtype,), call.device)
+        _check(out, "out", V.shape, (V.dtype,), call.index)
     call.run(_lib().gma_delta_decode, need,
              (ctypes.byref(desc), Qx.data_ptr(), Kx.data_ptr(), V.data_ptr(), g.data_ptr(), beta.data_ptr(),
               _ptr(lengths), _ptr(slots), pool, state.data_ptr(), out.data_ptr()), check_status)
@@ -249,8 +267,8 @@ def _cache(what, state, codes, scales, src, dst, stream, workspace):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dim() != 4:
             raise ValueError(f"{name} has {t.dim()} dimensions, expected 4")
-    dev = state.device
-    call = _Call(what, dev, stream, workspace)
+    call = _Call(what, state, stream, workspace)
+    dev = call.index
     S, H, R, cols = state.shape
     P = codes.shape[0]
     _check(state, "state", (S, H, R, cols), (torch.float32,), dev)
@@ -270,7 +288,7 @@ def gma_state_store(state, codes, scales, src=None, dst=None, workspace=None, st
     """Put carried states away in 8 bits: state[src[i]] -> codes[dst[i]], scales[dst[i]] for every i.
     state [S,H,R,C] float32 (the delta rule's [S,H,d,dv], gma_decode's [S,H,K,dv+1]), codes
     [P,H,R,C] int8, scales [P,H,R,ceil(C/32)] float32, src and dst int32 [n] (default i).  Groups
-    of 32 along a row share a scale max|x| / 127.  A negative index marks an absent entry; one
+    of 32 along a row share a scale max|x| * (1/127).  A negative index marks an absent entry; one
     outside its pool is skipped and posts GMA_ERR_BOUNDS; of several entries with one
     destination the last counts.  Returns (codes, scales)."""
     desc, call = _cache("gma_state_store", state, codes, scales, src, dst, stream, workspace)

@@ -403,8 +403,10 @@ gma_status gma_delta_decode(const gma_delta_desc *desc, const void *Qx, const vo
  * prefix).  A state is `rows` rows (heads times the rows of a head) of `cols`
  * float32 values: the delta rule's [H, d, dv] or gma_decode()'s [H, K, dv + 1].
  * Each row is cut into groups of 32 from its start, the last one maybe shorter:
- *   scale = max |x| / 127,  code = rint(x / scale)   (IEEE float32 divisions)
- * and reads back as code * scale; the error is at most max |x| / 254.  A group
+ *   scale = max |x| (1 / 127),  code = rint(x / scale)
+ * (float32: a product with the rounded 1 / 127, an IEEE division)
+ * and reads back as code * scale; the error is at most max |x| / 254 and
+ * three roundings.  A group
  * that holds a NaN or an infinity reads back as NaN.
  *   state  [n_states, rows, cols] float32     codes [n_cache, rows, cols] int8
  *   scales [n_cache, rows, ceil(cols / 32)] float32

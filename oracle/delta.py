@@ -57,7 +57,7 @@ def backward(Q, K, V, g, beta, scale, dO, state=None, dstate=None, lengths=None)
 
 
 def quantise(x):
-    """x [..., cols] float32 -> (codes int8, scales float32 [..., ceil(cols / 32)]): float32 quotients, as the format says."""
+    """x [..., cols] float32 -> (codes int8, scales float32 [..., ceil(cols / 32)]): in float32, as the format says."""
     cols = x.shape[-1]
     groups = -(-cols // 32)
     pad = np.zeros(x.shape[:-1] + (groups * 32,), np.float32)
@@ -65,7 +65,7 @@ def quantise(x):
     y = pad.reshape(x.shape[:-1] + (groups, 32))
     bad = ~np.isfinite(y).all(-1)
     y = np.where(bad[..., None], np.float32(0), y)
-    scale = np.abs(y).max(-1) / np.float32(127)
+    scale = np.abs(y).max(-1) * (np.float32(1) / np.float32(127))
     with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
         q = np.where(scale[..., None] > 0, y / scale[..., None], np.float32(0))
     codes = np.clip(np.rint(q), -127, 127).astype(np.int8)
