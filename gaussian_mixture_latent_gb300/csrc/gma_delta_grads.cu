@@ -101,10 +101,13 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
     for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) e[i][j] = 0.f;
+    auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+        for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    };
+    if (!ONE) clear();
     const int ar = (lane & 7) + ((lane >> 3) & 1) * 8, ac = lane >> 4;      // A operand, and B transposed: row, piece
     const int br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;      // B operand of two n tiles
     const int r0 = lane >> 2, q0 = 2 * (lane & 3);
@@ -126,9 +129,10 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
                 ldsm_t(g[0], st + at<L::kRow>(ks * 16 + ar, 2 * nd + ac));
                 ldsm_t(g[1], st + at<L::kRow>(ks * 16 + ar, 2 * nd + 2 + ac));
 #pragma unroll
-                for (int t = role ? 1 : 0; t >= 0; --t)
+                for (int t = 1; t >= 0; --t)
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
+                        if (t == 1 && role == 0) continue;
                         mma(acc[2 * (nd + m)], f[t], g[m][0], g[m][1]);
                         mma(acc[2 * (nd + m) + 1], f[t], g[m][2], g[m][3]);
                     }
@@ -185,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
                 }
             }
         }
+        if (ONE && role == 2) clear();
         if (!ONE || role == 2) state_product();
         if (role == 2) {
             for (int i = tid - 256; i < 64 * D / 2; i += 128) {      // <S, R>: both tiles have the same layout
@@ -274,7 +279,10 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
                 if (lane < 4) *reinterpret_cast<float2 *>(col + j) = make_float2(x, y);
             }
         }
-        if (ONE) state_product();
+        if (ONE) {
+            clear();                                     // only now: E's tiles and these never share the registers
+            state_product();
+        }
     }
     // row factors of the state's product, and its dot with q (k): one number a row
     const float m0 = role == 0 ? p.scale * vec.e[i0] : (role == 1 ? vec.e[i0] : vec.f[i0]) * vec.beta[i0];
