@@ -5,10 +5,10 @@
 //   dV = x,  dbeta_i = X_i . w_i
 //   dQ = scale diag(e^G) dO S^T + E1 K
 //   dK = -diag(e^G) x S^T - E2 K  +  E1^T Q - E2^T K + diag(e^{G_C - G}) U R^T
-//   dg_t = sum_{i >= t} a_i + sum_{j < t} b_j + e^{G_C} <S, R>, where with M = E1 o QK^T - E2 o KK^T
-//     a_i = M's row sum i - its column sum i + scale e^{G_i} q_i.S dO_i - e^{G_i} k_i.S x_i,  b_j = e^{G_C - G_j} k_j.R u_j
-// (pairs with both rows on one side of t cancel in the sums of a as the same fp32 numbers).
-//
+//   dg_t = sum_{i >= t} a_i + sum_{j < t} b_j + e^{G_C} <S, R>,  b_j = k_j . (the last term of dK)_j,
+//     a_i = q_i . dQ_i + k_i . (the first two terms of dK - the next two)_i,
+// in fp32 before dQ and dK are rounded.  A pair of rows on one side of t is in a twice, with both signs, by way of the
+// same terms of E and of bf16 q and k: what is left of it is rounding of fp32.
 // W and X come in two bf16 terms each; beta joins as a factor of rows and columns, and dbeta is the diagonal of X W^T.
 //
 // One CTA of twelve warps to a chunk, one warp of each role to a 16-row block.  First the four warps of role 0 make E1,
@@ -45,8 +45,8 @@ struct Smem {
     static constexpr int oVec = oE + 4 * kTriBytes, oRed = oVec + (int)sizeof(Vec);
     static constexpr int kPitch = D + 8;                 // floats: the exchange of dK's halves, over the slab's tiles
     static_assert(C * kPitch * 4 <= oE - oDo, "the exchange fits");
-    // sums: rows [64] and columns [4][64] of both matrices, b [64], dbeta [64], inner [12]
-    static constexpr int kRed = 64 + 64 + 256 + 256 + 64 + 64 + 16, total = oRed + kRed * 4;
+    // a's three parts and b [64] each, dbeta [64], inner [4]
+    static constexpr int kRed = 5 * 64 + 4, total = oRed + kRed * 4;
 };
 
 template <int D, bool ONE>
@@ -82,16 +82,8 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
     const __nv_bfloat16 *dO = static_cast<const __nv_bfloat16 *>(a.g.dO);
     const size_t plane = (size_t)p.B * p.H * p.N * p.dv;
     Vec &vec = *reinterpret_cast<Vec *>(sm + L::oVec);
-    float *row1 = reinterpret_cast<float *>(sm + L::oRed), *row2 = row1 + 64, *col1 = row2 + 64, *col2 = col1 + 256;
-    float *keys = col2 + 256, *dbeta = keys + 64, *inner = dbeta + 64;
+    float *sums = reinterpret_cast<float *>(sm + L::oRed), *keys = sums + 3 * 64, *dbeta = keys + 64, *inner = dbeta + 64;
 
-    for (int i = tid; i < C * (D / 8); i += kThreads) {
-        const int r = i / (D / 8), cc = i % (D / 8);
-        const bool ok = r < n && cc * 8 < p.d;
-        const size_t off = ok ? (krow + r) * p.d + cc * 8 : 0;
-        copy16(sb + at<L::kRow>(r, cc), K + off, ok);
-        copy16(sb + L::oQ + at<L::kRow>(r, cc), Q + off, ok);
-    }
     const char *chunk = a.g.chunks + ((size_t)bh * a.nc + c) * a.chunk_bytes + a.vec_at;
     if (tid < (int)sizeof(Vec) / 16) copy16(sb + L::oVec + 16 * tid, chunk + 16 * tid, true);
     const __nv_bfloat16 *s0 = a.g.s0 + ((size_t)bh * a.nc + c) * p.dv * p.d, *ds = a.g.ds + ((size_t)bh * a.nc + c) * p.dv * p.d;
@@ -145,20 +137,25 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
             const int r = i / 8, cc = i % 8;
             const bool ok = r < n && v0 + cc * 8 < p.dv;
             const size_t off = ok ? (vrow + r) * p.dv + v0 + cc * 8 : 0;
-            const uint32_t to = at<128>(r, cc);
-            copy16(ot + to, dO + off, ok);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                copy16(wt + t * L::kSlab + to, a.g.w + t * plane + off, ok);
-                copy16(xt + t * L::kSlab + to, a.g.x + t * plane + off, ok);
-            }
+            const uint32_t to = sb + at<128>(r, cc);
+            copy16(to + L::oDo, dO + off, ok);
+            copy16(to + L::oW, a.g.w + off, ok);
+            copy16(to + L::oW + L::kSlab, a.g.w + plane + off, ok);
+            copy16(to + L::oX, a.g.x + off, ok);
+            copy16(to + L::oX + L::kSlab, a.g.x + plane + off, ok);
         }
-        for (int i = tid; i < 64 * (D / 8); i += kThreads) {
+        for (int i = tid; i < C * (D / 8); i += kThreads) {          // 64 rows of q and k, 64 columns of the states
             const int r = i / (D / 8), cc = i % (D / 8);
-            const bool ok = v0 + r < p.dv && cc * 8 < p.d;
-            const size_t off = ok ? (size_t)(v0 + r) * p.d + cc * 8 : 0;
-            copy16(sb + L::oS + at<L::kRow>(r, cc), s0 + off, ok);
-            copy16(sb + L::oR + at<L::kRow>(r, cc), ds + off, ok);
+            const bool in = cc * 8 < p.d, row = in && r < n, dim = in && v0 + r < p.dv;
+            const uint32_t to = sb + at<L::kRow>(r, cc);
+            if (v0 == 0) {
+                const size_t off = row ? (krow + r) * p.d + cc * 8 : 0;
+                copy16(to, K + off, row);
+                copy16(to + L::oQ, Q + off, row);
+            }
+            const size_t off = dim ? (size_t)(v0 + r) * p.d + cc * 8 : 0;
+            copy16(to + L::oS, s0 + off, dim);
+            copy16(to + L::oR, ds + off, dim);
         }
         copy_commit();
         copy_wait<0>();
@@ -213,100 +210,76 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
     }
     const int i0 = rb * 16 + r0, i1 = i0 + 8;
     const uint32_t et = sb + L::oE;
-    float d0 = 0.f, d1 = 0.f;
     if (role < 2) {
-        // E's decays, factors and masks; M = E o (Q or K) K^T: row sums and column sums; E's terms to shared memory
-        const float2 g0 = vec.G[i0], g1 = vec.G[i1];
-        const float2 gr = vec.G[rb * 16];
+        // E's decays, factors and masks, and its terms to shared memory
+        const float2 g0 = vec.G[i0], g1 = vec.G[i1], gr = vec.G[rb * 16];
         const float m0 = role ? vec.beta[i0] : p.scale, m1 = role ? vec.beta[i1] : p.scale;
         const float a0 = m0 * ex2((g0.x - gr.x) + (g0.y - gr.y)), a1 = m1 * ex2((g1.x - gr.x) + (g1.y - gr.y));
-        float *col = (role ? col2 : col1) + 64 * rb;
-        char *to = sm + L::oE + 2 * role * kTriBytes;
-        const uint32_t left = sb + (role == 0 ? L::oQ : 0);
+        char *to = sm + L::oE + 2 * role * kTriBytes + 4 * (lane & 3);
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-            float qk[2][4] = {};
-            if (np <= rb) {
+        for (int t = 0; t < 8; ++t) {
+            const int np = t / 2, j = 8 * t + q0;
+            if (np > rb) continue;
+            const float4 gj = *reinterpret_cast<const float4 *>(vec.G + j);
+            const float2 bj = *reinterpret_cast<const float2 *>(vec.beta + j);
+            if (np < rb) {
+                // the decay by way of the row block's first row: both factors' exponents are <= 0
+                const float bx = bj.x * ex2((gr.x - gj.x) + (gr.y - gj.y)), by = bj.y * ex2((gr.x - gj.z) + (gr.y - gj.w));
+                e[t][0] *= a0 * bx; e[t][1] *= a0 * by; e[t][2] *= a1 * bx; e[t][3] *= a1 * by;
+            } else {
+                const float dd[4] = {ex2((g0.x - gj.x) + (g0.y - gj.y)) * (m0 * bj.x), ex2((g0.x - gj.z) + (g0.y - gj.w)) * (m0 * bj.y),
+                                     ex2((g1.x - gj.x) + (g1.y - gj.y)) * (m1 * bj.x), ex2((g1.x - gj.z) + (g1.y - gj.w)) * (m1 * bj.y)};
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    uint32_t f[4], g[4];
-                    ldsm(f, left + at<L::kRow>(rb * 16 + ar, 2 * ks + ac));
-                    ldsm(g, sb + at<L::kRow>(np * 16 + br, 2 * ks + bc));
-                    mma(qk[0], f, g[0], g[1]);
-                    mma(qk[1], f, g[2], g[3]);
+                for (int m = 0; m < 4; ++m) {
+                    const int i = m < 2 ? i0 : i1, jj = j + (m & 1);
+                    if (role && jj == i) dbeta[i] = e[t][m];
+                    // a select and not a product with 0: what lies outside the triangle may be infinite
+                    e[t][m] = (role ? jj >= i : jj > i) ? 0.f : e[t][m] * dd[m];
                 }
             }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = 2 * np + u, j = 8 * t + q0;
-                float x = 0.f, y = 0.f;
-                if (np <= rb) {
-                    const float4 gj = *reinterpret_cast<const float4 *>(vec.G + j);
-                    const float2 bj = *reinterpret_cast<const float2 *>(vec.beta + j);
-                    if (np < rb) {
-                        // the decay by way of the row block's first row: both factors' exponents are <= 0
-                        const float bx = bj.x * ex2((gr.x - gj.x) + (gr.y - gj.y)), by = bj.y * ex2((gr.x - gj.z) + (gr.y - gj.w));
-                        e[t][0] *= a0 * bx; e[t][1] *= a0 * by; e[t][2] *= a1 * bx; e[t][3] *= a1 * by;
-                    } else {
-                        const float dd[4] = {ex2((g0.x - gj.x) + (g0.y - gj.y)) * (m0 * bj.x), ex2((g0.x - gj.z) + (g0.y - gj.w)) * (m0 * bj.y),
-                                             ex2((g1.x - gj.x) + (g1.y - gj.y)) * (m1 * bj.x), ex2((g1.x - gj.z) + (g1.y - gj.w)) * (m1 * bj.y)};
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const int i = m < 2 ? i0 : i1, jj = j + (m & 1);
-                            if (role && jj == i) dbeta[i] = e[t][m];
-                            // a select and not a product with 0: what lies outside the triangle may be infinite
-                            e[t][m] = (role ? jj >= i : jj > i) ? 0.f : e[t][m] * dd[m];
-                        }
-                    }
-                    const float s0 = e[t][0] * qk[u][0], s1 = e[t][1] * qk[u][1], s2 = e[t][2] * qk[u][2], s3 = e[t][3] * qk[u][3];
-                    d0 += s0 + s1;
-                    d1 += s2 + s3;
-                    x = s0 + s2;
-                    y = s1 + s3;
-                    for (int o = 4; o < 32; o <<= 1) {
-                        x += __shfl_xor_sync(~0u, x, o);
-                        y += __shfl_xor_sync(~0u, y, o);
-                    }
-                    uint32_t w[2];
-                    const uint32_t blk = tri(rb, np) + 4 * (lane & 3);
-                    split<2>(e[t][0], e[t][1], w);
-                    *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0, u)) = w[0];
-                    *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0, u) + kTriBytes) = w[1];
-                    split<2>(e[t][2], e[t][3], w);
-                    *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0 + 8, u)) = w[0];
-                    *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0 + 8, u) + kTriBytes) = w[1];
-                }
-                if (lane < 4) *reinterpret_cast<float2 *>(col + j) = make_float2(x, y);
-            }
+            uint32_t w[2];
+            const uint32_t blk = tri(rb, np);
+            split<2>(e[t][0], e[t][1], w);
+            *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0, t & 1)) = w[0];
+            *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0, t & 1) + kTriBytes) = w[1];
+            split<2>(e[t][2], e[t][3], w);
+            *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0 + 8, t & 1)) = w[0];
+            *reinterpret_cast<uint32_t *>(to + blk + at<32>(r0 + 8, t & 1) + kTriBytes) = w[1];
         }
         if (ONE) {
             clear();                                     // only now: E's tiles and these never share the registers
             state_product();
         }
     }
-    // row factors of the state's product, and its dot with q (k): one number a row
-    const float m0 = role == 0 ? p.scale * vec.e[i0] : (role == 1 ? vec.e[i0] : vec.f[i0]) * vec.beta[i0];
-    const float m1 = role == 0 ? p.scale * vec.e[i1] : (role == 1 ? vec.e[i1] : vec.f[i1]) * vec.beta[i1];
-    const char *own = sm + (role == 0 ? L::oQ : 0);
+    // row factors of the state's product; dK takes its query half with the other sign
+    {
+        const float m0 = role == 0 ? p.scale * vec.e[i0] : (role == 1 ? -vec.e[i0] : vec.f[i0]) * vec.beta[i0];
+        const float m1 = role == 0 ? p.scale * vec.e[i1] : (role == 1 ? -vec.e[i1] : vec.f[i1]) * vec.beta[i1];
 #pragma unroll
-    for (int t = 0; t < D / 8; ++t) {
-        acc[t][0] *= m0; acc[t][1] *= m0; acc[t][2] *= m1; acc[t][3] *= m1;
-        const uint32_t x = *reinterpret_cast<const uint32_t *>(own + at<L::kRow>(i0, t) + 2 * q0);
-        const uint32_t y = *reinterpret_cast<const uint32_t *>(own + at<L::kRow>(i1, t) + 2 * q0);
-        d0 = fmaf(acc[t][0], low(x), fmaf(acc[t][1], high(x), d0));
-        d1 = fmaf(acc[t][2], low(y), fmaf(acc[t][3], high(y), d1));
-        if (role == 1)                                   // dK takes its query half with the other sign
+        for (int t = 0; t < D / 8; ++t) {
+            acc[t][0] *= m0; acc[t][1] *= m0; acc[t][2] *= m1; acc[t][3] *= m1;
+        }
+    }
+    // the rows' dots with q (role 0) or k
+    auto dots = [&](float *to) {
+        const char *own = sm + (role == 0 ? L::oQ : 0);
+        float d0 = 0.f, d1 = 0.f;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) acc[t][m] = -acc[t][m];
-    }
-    d0 += __shfl_xor_sync(~0u, d0, 1); d0 += __shfl_xor_sync(~0u, d0, 2);
-    d1 += __shfl_xor_sync(~0u, d1, 1); d1 += __shfl_xor_sync(~0u, d1, 2);
-    float *line = role == 0 ? row1 : role == 1 ? row2 : keys;
-    if ((lane & 3) == 0) {
-        line[i0] = d0;
-        line[i1] = d1;
-    }
+        for (int t = 0; t < D / 8; ++t) {
+            const uint32_t x = *reinterpret_cast<const uint32_t *>(own + at<L::kRow>(i0, t) + 2 * q0);
+            const uint32_t y = *reinterpret_cast<const uint32_t *>(own + at<L::kRow>(i1, t) + 2 * q0);
+            d0 = fmaf(acc[t][0], low(x), fmaf(acc[t][1], high(x), d0));
+            d1 = fmaf(acc[t][2], low(y), fmaf(acc[t][3], high(y), d1));
+        }
+        d0 += __shfl_xor_sync(~0u, d0, 1); d0 += __shfl_xor_sync(~0u, d0, 2);
+        d1 += __shfl_xor_sync(~0u, d1, 1); d1 += __shfl_xor_sync(~0u, d1, 2);
+        if ((lane & 3) == 0) {
+            to[i0] = d0;
+            to[i1] = d1;
+        }
+    };
     if (role == 2) {
+        dots(keys);
         for (int o = 16; o; o >>= 1) in += __shfl_xor_sync(~0u, in, o);
         if (lane == 0) inner[rb] = in;
     }
@@ -348,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
         if (role == 2) add_e(0, false, sb + L::oQ);
         add_e(1, true, sb);
     }
+    dots(sums + 64 * role);
     float *half = reinterpret_cast<float *>(sm + L::oDo);            // the slabs are done with
     // rows i0 and i1 of dQ or dK
     auto store_rows = [&](__nv_bfloat16 *out, float *heads) {
@@ -385,16 +359,14 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
         store_rows(dK, a.g.dk_heads);
     }
     if (warp == 0) {
-        // a: rows and columns of both matrices; running sums from the end of a, from the start of b (two rows to a lane)
-        float av[2], bv[2], tot = 0.f;
-        for (int w = 0; w < 4; ++w) tot += inner[w];
+        // running sums from the end of a, from the start of b (two rows to a lane)
+        float av[2], bv[2];
+        const float tot = (inner[0] + inner[1]) + (inner[2] + inner[3]);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const int i = 2 * lane + m;
-            float x = row1[i] - row2[i];
-            for (int w = 0; w < 4; ++w) x -= col1[64 * w + i] - col2[64 * w + i];
-            av[m] = x;
             bv[m] = keys[i];
+            av[m] = (sums[i] + sums[64 + i]) - (sums[128 + i] - bv[m]);      // the key half without its last term
         }
         float after = av[0] + av[1], before = bv[0] + bv[1];
         for (int o = 1; o < 32; o <<= 1) {
