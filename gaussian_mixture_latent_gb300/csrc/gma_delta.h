@@ -99,10 +99,10 @@ __device__ __forceinline__ void delta_gate_out(void *p, size_t i, float v, bool 
 __device__ __forceinline__ int delta_len(const int *lengths, int b, int N) {
     return lengths ? min(max(lengths[b], 0), N) : N;
 }
-// A log decay at or below -1e5 forgets everything (e^g = 0 in fp32); holding it there keeps sums of a chunk's
-// decays finite, so that minus infinity and the type's lowest value are ordinary inputs.  The same above (e^g is
+// A log decay below -1024 forgets everything (e^g = 0 in fp32, from about -104 on); holding it there keeps sums of a
+// chunk's decays finite, so that minus infinity and the type's lowest value are ordinary inputs.  The same above (e^g is
 // infinite).  NaN passes through.
-__device__ __forceinline__ float delta_floor(float g) { return g < -1e5f ? -1e5f : g > 1e5f ? 1e5f : g; }
+__device__ __forceinline__ float delta_floor(float g) { return g < -1024.f ? -1024.f : g > 1024.f ? 1024.f : g; }
 #endif
 
 }  // namespace gma

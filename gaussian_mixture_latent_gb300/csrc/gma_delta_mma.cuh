@@ -134,16 +134,16 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Running sums of 64 base-2 log decays (two rows to a lane of one warp) as pairs of floats (hi + lo).  The sums are in
-// 32.32 fixed point: exact, so that a difference of two of them is good to 2^-32 however large they are (fp64 adds
-// would do, but cost 2000 cycles here).  A NaN decay makes its row and those after it NaN.
+// fixed point with 44 bits after the point (64 times 1024 log2(e) takes 17 before it): exact, so that a difference of two
+// of them is good to 2^-44 however large they are (fp64 adds would do, but cost 2000 cycles here).
 __device__ __forceinline__ long long fixed_log2(float g) {
     const float l2 = 1.44269502f, l2lo = 1.92596299e-8f;      // log2(e) in two floats
     const float x = g * l2, y = fmaf(g, l2, -x) + g * l2lo;
-    return __float2ll_rn(x * 4294967296.f) + __float2ll_rn(y * 4294967296.f);
+    return __float2ll_rn(x * 0x1p44f) + __float2ll_rn(y * 0x1p44f);
 }
 __device__ __forceinline__ float2 fixed_pair(long long q) {
     const float hi = __ll2float_rn(q);
-    return make_float2(hi * 0x1p-32f, __ll2float_rn(q - __float2ll_rn(hi)) * 0x1p-32f);
+    return make_float2(hi * 0x1p-44f, __ll2float_rn(q - __float2ll_rn(hi)) * 0x1p-44f);
 }
 
 template <int V>

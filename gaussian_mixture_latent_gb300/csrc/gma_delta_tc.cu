@@ -266,7 +266,8 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kern
 // KS > 1: the warps split the first product's sum (their parts of d), then the 64 rows (eight-row tiles r, 7 - r, ..: the
 // same work under the triangles), then the columns of S^T; in between they exchange partial sums, R and U through shared
 // memory, lane by lane.
-// A helper warp to each slice takes what the next chunk does not wait for.  kFwd: O, from the state (one bf16 term) and U
+// As many helper warps to a slice take what the next chunk does not wait for, each for the same tiles of eight rows (or its
+// part of d).  kFwd: O, from the state (one bf16 term) and U
 // that the chain leaves in shared memory.  kCkpt and kBack: the stores; kBack also the products of dO with P and Q, which
 // the chain adds.  Four loader warps copy chunk c + kStages - 1 while chunk c is worked on.
 //
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kern
 // but its accumulators are in TMEM: three dependent products a chunk would each pay a round trip (load, split, store,
 // fence, issue) of about a chunk's time here.
 enum Mode { kFwd, kCkpt, kBack };
-constexpr int kGroup = 128;            // threads of the chain, of the helpers (SL of the four warps work), of the loaders
+constexpr int kGroup = 128;            // threads of the chain, of the helpers, of the loaders
 // Registers: launched with 168 a thread, 3 x 128 x 168 = 64512 = 128 x (240 + 192 + 72).
 constexpr int kChainRegs = 240, kHelpRegs = 192, kLoadRegs = 72;
 enum { kBarAll = 1, kBarSlice = 2, kBarU = 6, kBarZ = 10 };          // named barriers; one each of the last three to a slice
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
     using L = ChainSmem<D, NT, SL, MODE>;
     using W = Chunk<NT>;
     constexpr int KS = L::KS, DK = D / KS, OWN = 8 / KS;
-    constexpr int kAll = 2 * kGroup + 32 * SL;           // the chain, the helpers at work, the loaders
+    constexpr int kAll = 3 * kGroup, kPair = 64 * KS;    // threads of the CTA; of a slice's chain and helpers
     constexpr bool BACK = MODE == kBack;
     extern __shared__ __align__(128) char sm[];
     const DeltaProblem &p = a.p;
@@ -472,16 +473,19 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
     float4 *zp = reinterpret_cast<float4 *>(mine + L::oZ), *zq = zp + 8 * 32;       // kBack
     const int q0 = 2 * (lane & 3), br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;   // B operand: row, piece
     const int col = c0 + 16 * slice + (lane >> 2);
+    // the warp's eight-row tiles: all, or r, 7 - r (and r + 2, 5 - r of two warps)
+    auto own = [&](int j) {
+        return KS == 1 ? j : j == 0 ? rank : j == 1 ? 7 - rank : j == 2 ? rank + 2 : 5 - rank;
+    };
 
     if (tid >= kGroup) {
         // ---------------------------------------------------------------------------------------- helpers
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHelpRegs));
-        if (warp - 4 >= SL) return;
-        // [16 columns, 64 rows] in packed pairs of rows as bf16 rows, through the chunk's own V columns, to memory
-        auto to_memory = [&](__nv_bfloat16 *to, int c, char *st, const uint32_t (&x)[8][2]) {
+        // the tiles [16 columns, 8 rows] in packed pairs of rows as bf16 rows, through the chunk's own V columns, to memory
+        auto to_memory = [&](__nv_bfloat16 *to, int c, char *st, const uint32_t (&x)[OWN][2]) {
 #pragma unroll
-            for (int n = 0; n < 8; n += 2) {
-                const int r = 8 * n + br;
+            for (int n = 0; n < OWN; n += 2) {
+                const int r = (lane >> 4 ? own(n + 1) : own(n)) * 8 + (lane & 7);
                 char *at_r = st + L::oV + at<L::kValRow>(r, 2 * slice + bc);
                 stsm_t(smem_u32(at_r), x[n][0], x[n][1], x[n + 1][0], x[n + 1][1]);
                 __syncwarp();
@@ -497,8 +501,8 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             char *st = sm + (ci % L::kStages) * L::kStage;
             const uint32_t qt = smem_u32(st) + L::oQ, vt = smem_u32(st) + L::oV, pt = smem_u32(st) + L::oW + W::oP;
             const Vec &vec = *reinterpret_cast<const Vec *>(st + L::oW + W::oVec);
-            float x[8][4];
-            uint4 was[D / 16];
+            float x[OWN][4];
+            uint4 was[DK / 16];
             zero(x);
             if (MODE == kFwd) {
                 // O = scale e^G Q S, then + P U
@@ -507,17 +511,17 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
                     const uint4 s4 = held[ks * 32 + lane];
                     const uint32_t fs[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-                    for (int np = 0; np < 4; ++np) {
+                    for (int j = 0; j < OWN; j += 2) {
                         uint32_t fq[4];
-                        ldsm(fq, qt + at<L::kRow>(np * 16 + br, 2 * ks + bc));
-                        mma(x[2 * np], fs, fq[0], fq[1]);
-                        mma(x[2 * np + 1], fs, fq[2], fq[3]);
+                        ldsm(fq, qt + at<L::kRow>((lane >> 4 ? own(j + 1) : own(j)) * 8 + (lane & 7), 2 * ks + bc));
+                        mma(x[j], fs, fq[0], fq[1]);
+                        mma(x[j + 1], fs, fq[2], fq[3]);
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const float2 e = pair(vec.e + 8 * n + q0);
-                    scale_cols(x[n], make_float2(p.scale * e.x, p.scale * e.y));
+                for (int j = 0; j < OWN; ++j) {
+                    const float2 e = pair(vec.e + 8 * own(j) + q0);
+                    scale_cols(x[j], make_float2(p.scale * e.x, p.scale * e.y));
                 }
             } else {
                 if (BACK) {
@@ -525,13 +529,13 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
                     uint32_t fd[4][1][4];
 #pragma unroll
                     for (int kb = 0; kb < 4; ++kb) ldsm_t(fd[kb][0], vt + at<L::kValRow>(kb * 16 + br, 2 * slice + bc));
-                    triangle<true, 2, 1>(x, fd, pt, lane, [](int j) { return j; }, [](int) {});
+                    triangle<true, 2, 1>(x, fd, pt, lane, own, [](int) {});
 #pragma unroll
-                    for (int n = 0; n < 8; ++n) zp[n * 32 + lane] = as4(x[n]);
-                    bar<32 * (KS + 1)>(kBarZ + slice);
-                    float y[D / 8][4];
+                    for (int j = 0; j < OWN; ++j) zp[own(j) * 32 + lane] = as4(x[j]);
+                    bar<kPair>(kBarZ + slice);
+                    float y[DK / 8][4];
                     zero(y);
-                    add_outer<L::kRow, NT>(y, qt, 0, lane, [&](int kb, float (&z0)[4], float (&z1)[4]) {
+                    add_outer<L::kRow, NT>(y, qt, rank * DK / 8, lane, [&](int kb, float (&z0)[4], float (&z1)[4]) {
                         const uint32_t (&o)[4] = fd[kb][0];
                         const float2 e0 = pair(vec.e + 16 * kb + q0), e1 = pair(vec.e + 16 * kb + 8 + q0);
                         z0[0] = low(o[0]); z0[1] = high(o[0]); z0[2] = low(o[1]); z0[3] = high(o[1]);
@@ -540,55 +544,53 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
                         scale_cols(z1, make_float2(p.scale * e1.x, p.scale * e1.y));
                     });
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n) zq[n * 32 + lane] = as4(y[n]);
+                    for (int n = 0; n < DK / 8; ++n) zq[(rank * DK / 8 + n) * 32 + lane] = as4(y[n]);
                 }
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) was[ks] = held[ks * 32 + lane];
+                for (int ks = 0; ks < DK / 16; ++ks) was[ks] = held[(rank * DK / 16 + ks) * 32 + lane];
             }
-            bar<32 * (KS + 1)>(kBarU + slice);           // U is there; the chain may change `held`
-            float z[8][4];
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                const float4 y = reinterpret_cast<const float4 *>(rows)[n * 32 + lane];
-                z[n][0] = y.x; z[n][1] = y.y; z[n][2] = y.z; z[n][3] = y.w;
-            }
+            bar<kPair>(kBarU + slice);                   // U is there; the chain may change `held`
             if (MODE == kFwd) {
-                uint32_t fu[4][2][4], o[8][2];
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) split_a<2>(z[2 * kb], z[2 * kb + 1], fu[kb]);
-                triangle<false, 2, 1>(x, fu, pt, lane, [](int j) { return j; }, [&](int u) {
-                    const int kb = 2 + u / 2;
-                    split_quarter<2>(z[2 * kb], z[2 * kb + 1], fu[kb], 2 * (u & 1));
-                    split_quarter<2>(z[2 * kb], z[2 * kb + 1], fu[kb], 2 * (u & 1) + 1);
-                });
+                float z[8][4];
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
-                    o[n][0] = pack(x[n][0], x[n][1]);
-                    o[n][1] = pack(x[n][2], x[n][3]);
+                    const float4 y = reinterpret_cast<const float4 *>(rows)[n * 32 + lane];
+                    z[n][0] = y.x; z[n][1] = y.y; z[n][2] = y.z; z[n][3] = y.w;
+                }
+                uint32_t fu[4][2][4], o[OWN][2];
+#pragma unroll
+                for (int kb = 0; kb < 4; ++kb) split_a<2>(z[2 * kb], z[2 * kb + 1], fu[kb]);
+                triangle<false, 2, 1>(x, fu, pt, lane, own, [](int) {});
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) {
+                    o[j][0] = pack(x[j][0], x[j][1]);
+                    o[j][1] = pack(x[j][2], x[j][3]);
                 }
                 to_memory(static_cast<__nv_bfloat16 *>(a.out), c, st, o);
             } else {
                 // the state as it was held: [dv, d] in bf16
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
+                for (int ks = 0; ks < DK / 16; ++ks) {
                     const uint32_t s2[4] = {was[ks].x, was[ks].y, was[ks].z, was[ks].w};
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
-                        const int r = 16 * ks + 8 * (m >> 1) + q0, cc = col + 8 * (m & 1);
+                        const int r = rank * DK + 16 * ks + 8 * (m >> 1) + q0, cc = col + 8 * (m & 1);
                         if (r < p.d && cc < p.dv)
                             *reinterpret_cast<uint32_t *>(a.states + (((size_t)bh * a.nc + c) * p.dv + cc) * p.d + r) = s2[m];
                     }
                 }
                 // W = U / beta (X as it is) in two terms
-                uint32_t t0[8][2], t1[8][2];
+                uint32_t t0[OWN][2], t1[OWN][2];
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    if (!BACK) scale_cols(z[n], pair(vec.ibeta + 8 * n + q0));
+                for (int j = 0; j < OWN; ++j) {
+                    const float4 y = reinterpret_cast<const float4 *>(rows)[own(j) * 32 + lane];
+                    float z[4] = {y.x, y.y, y.z, y.w};
+                    if (!BACK) scale_cols(z, pair(vec.ibeta + 8 * own(j) + q0));
                     uint32_t t[2];
-                    split<2>(z[n][0], z[n][1], t);
-                    t0[n][0] = t[0]; t1[n][0] = t[1];
-                    split<2>(z[n][2], z[n][3], t);
-                    t0[n][1] = t[0]; t1[n][1] = t[1];
+                    split<2>(z[0], z[1], t);
+                    t0[j][0] = t[0]; t1[j][0] = t[1];
+                    split<2>(z[2], z[3], t);
+                    t0[j][1] = t[0]; t1[j][1] = t[1];
                 }
                 to_memory(a.rows, c, st, t0);
                 to_memory(a.rows + (size_t)p.B * p.H * p.N * p.dv, c, st, t1);
@@ -616,10 +618,6 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             held[(k0 / 16 + ks) * 32 + lane] = make_uint4(pack(S[2 * ks][0], S[2 * ks][1]), pack(S[2 * ks][2], S[2 * ks][3]),
                                                           pack(S[2 * ks + 1][0], S[2 * ks + 1][1]),
                                                           pack(S[2 * ks + 1][2], S[2 * ks + 1][3]));
-    };
-    // the warp's eight-row tiles: all, or r, 7 - r (and r + 2, 5 - r of two warps)
-    auto own = [&](int j) {
-        return KS == 1 ? j : j == 0 ? rank : j == 1 ? 7 - rank : j == 2 ? rank + 2 : 5 - rank;
     };
     auto meet = [&] { if (KS > 1) bar<32 * KS>(kBarSlice + slice); };
     hold();
@@ -668,7 +666,7 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             x[j][0] = s4.x; x[j][1] = s4.y; x[j][2] = s4.z; x[j][3] = s4.w;
         }
         // R = beta (V - e^G K S), kBack: dU = f K R + P^T dO, a pair of tiles at a time
-        if (BACK) bar<32 * (KS + 1)>(kBarZ + slice);
+        if (BACK) bar<kPair>(kBarZ + slice);
         auto right_side = [&](int j) {
             if (BACK) {
 #pragma unroll
@@ -736,7 +734,7 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
         }
 #pragma unroll
         for (int j = 0; j < OWN; ++j) reinterpret_cast<float4 *>(rows)[own(j) * 32 + lane] = as4(u[j]);
-        bar<32 * (KS + 1)>(kBarU + slice);
+        bar<kPair>(kBarU + slice);
         // S <- e^{G_C} S + (f U)^T K  (kBack: R <- e^{G_C} R + the helper's part - (e^G beta X)^T K)
         const float last = vec.last;
 #pragma unroll

@@ -221,6 +221,8 @@ def gma_delta_backward(Qx, Kx, V, g, beta, dO, state=None, dstate=None, lengths=
         if t is not None:
             _check(t, name, shape, (torch.float32,), call.index)
     inputs = (Qx, Kx, V, g, beta, state)
+    if grads is not None and len(grads) != 6:
+        raise ValueError(f"grads has {len(grads)} entries, expected 6")
     if grads is None:
         grads = tuple(None if t is None else call.empty(t.shape, t.dtype) for t in inputs)
     else:

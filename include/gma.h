@@ -350,8 +350,8 @@ gma_status gma_project(const gma_proj_desc *desc, const void *X, const void *Wq,
  *   lengths [B] int32 or NULL: rows at and past lengths[b] (held to [0, N]) do
  *     not exist: their inputs are not used, out and every gradient is 0 there.
  * d, dv from 1 to 256; H a multiple of Hk.  g is a log decay, normally <= 0;
- * minus infinity or a very low value (below -1e5) forgets the state (a document
- * boundary).  The recurrence is stable while beta |Kx|^2 <= 2.  beta = 0 with
+ * minus infinity or any value whose e^g is 0 in float32 (below about -104)
+ * forgets the state (a document boundary).  The recurrence is stable while beta |Kx|^2 <= 2.  beta = 0 with
  * g = 0 leaves the state as it is.  A NaN or an infinity in a row may reach
  * rows of the same 64-row chunk before it.
  */

@@ -228,6 +228,22 @@ def test_forward(gma, shape, dtype, gates):
     check_forward(gma, x, dtype)
 
 
+# heads and dv from one CTA to 16 columns to one to 64, at both widths: the same rule as a few heads, and for the backward
+MANY = [(2, 20, 10, 150, 64, 64), (3, 30, 30, 130, 64, 128), (5, 8, 4, 140, 128, 128), (3, 10, 10, 200, 128, 128),
+        (1, 90, 90, 100, 128, 64), (2, 25, 25, 129, 96, 72), (3, 25, 25, 70, 48, 200)]
+
+
+@gpu
+@pytest.mark.parametrize("gates", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", MANY, ids=str)
+def test_many_heads(gma, shape, gates):
+    B, H, Hk, N, d, dv = shape
+    lengths = [N, N - 37, 0, 64, 1][:B]
+    check_forward(gma, make(B, H, N, d, dv, "bf16", gates, Hk=Hk, seed=N, state=True, lengths=lengths), "bf16")
+    check_backward(gma, make(B, H, N, d, dv, "bf16", gates, Hk=Hk, seed=N, state=True, lengths=lengths), "bf16", gates)
+    check_backward(gma, make(B, H, N, d, dv, "bf16", gates, Hk=Hk, seed=N + 1), "bf16", gates)
+
+
 @gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (24, 20)])
