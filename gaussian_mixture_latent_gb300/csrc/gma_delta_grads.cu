@@ -16,8 +16,9 @@
 // U R^T; then role 0 makes dQ, role 1 the query half of dK and role 2 the key half from the same E tiles, read transposed.
 // dv goes by in slabs of 64 columns; with one slab (ONE) the states' products wait until E is done, which leaves 80
 // registers a thread and two CTAs to an SM.
-// Precision: W, X and E in two bf16 terms (2^-17), the two states in one: half a bf16 step of their products, as the
-// gradients' own rounding.  Bound by the latency of few warps between barriers; the mma.sync issue alone is about
+// Precision: W, X, E and S in two bf16 terms (2^-17), R in one: half a bf16 step of its products, as the gradients' own
+// rounding.  (With S in one term too, dg, which adds and subtracts all of these, was 2.6e-3 off against the 1.7e-3 that
+// rounding it to bf16 costs.)  Bound by the latency of few warps between barriers; the mma.sync issue alone is about
 // 3700 cycles a chunk at 64 x 64 (8 cycles each on a tensor unit).
 #include <cstdint>
 
@@ -40,7 +41,7 @@ struct Args {
 template <int D>
 struct Smem {
     static constexpr int kRow = 2 * D, kKey = C * kRow, kSlab = C * 128;
-    static constexpr int oQ = kKey, oDo = 2 * kKey, oW = oDo + kSlab, oX = oW + 2 * kSlab, oS = oX + 2 * kSlab, oR = oS + kKey;
+    static constexpr int oQ = kKey, oDo = 2 * kKey, oW = oDo + kSlab, oX = oW + 2 * kSlab, oS = oX + 2 * kSlab, oR = oS + 2 * kKey;
     static constexpr int oE = oR + kKey;                 // E1 and E2, two terms each, as packed triangles
     static constexpr int oVec = oE + 4 * kTriBytes, oRed = oVec + (int)sizeof(Vec);
     static constexpr int kPitch = D + 8;                 // floats: the exchange of dK's halves, over the slab's tiles
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
     }
     const __nv_bfloat16 *K = static_cast<const __nv_bfloat16 *>(p.Kx), *Q = static_cast<const __nv_bfloat16 *>(p.Qx);
     const __nv_bfloat16 *dO = static_cast<const __nv_bfloat16 *>(a.g.dO);
-    const size_t plane = (size_t)p.B * p.H * p.N * p.dv;
+    const size_t plane = (size_t)p.B * p.H * p.N * p.dv, states = (size_t)p.B * p.H * a.nc * p.dv * p.d;
     Vec &vec = *reinterpret_cast<Vec *>(sm + L::oVec);
     float *sums = reinterpret_cast<float *>(sm + L::oRed), *keys = sums + 3 * 64, *dbeta = keys + 64, *inner = dbeta + 64;
 
@@ -114,12 +115,22 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
             uint32_t f[2][4];
             ldsm(f[0], left + at<128>(rb * 16 + ar, 2 * ks + ac));
             if (role) ldsm(f[1], left + L::kSlab + at<128>(rb * 16 + ar, 2 * ks + ac));
-            // four tiles of one term, then of the other: an accumulator is used again after three other products
+            // four tiles of one product, then of the next: an accumulator is used again after three others
 #pragma unroll
             for (int nd = 0; nd < D / 16; nd += 2) {
-                uint32_t g[2][4];
-                ldsm_t(g[0], st + at<L::kRow>(ks * 16 + ar, 2 * nd + ac));
-                ldsm_t(g[1], st + at<L::kRow>(ks * 16 + ar, 2 * nd + 2 + ac));
+                uint32_t g[2][4], lo[2][4];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const uint32_t o = st + at<L::kRow>(ks * 16 + ar, 2 * (nd + m) + ac);
+                    ldsm_t(g[m], o);
+                    if (role < 2) ldsm_t(lo[m], o + L::kKey);
+                }
+                if (role < 2)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        mma(acc[2 * (nd + m)], f[0], lo[m][0], lo[m][1]);
+                        mma(acc[2 * (nd + m) + 1], f[0], lo[m][2], lo[m][3]);
+                    }
 #pragma unroll
                 for (int t = 1; t >= 0; --t)
 #pragma unroll
@@ -155,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
             }
             const size_t off = dim ? (size_t)(v0 + r) * p.d + cc * 8 : 0;
             copy16(to + L::oS, s0 + off, dim);
+            copy16(to + L::oS + L::kKey, s0 + states + off, dim);
             copy16(to + L::oR, ds + off, dim);
         }
         copy_commit();
@@ -189,10 +201,11 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
         if (ONE && role == 2) clear();
         if (!ONE || role == 2) state_product();
         if (role == 2) {
-            for (int i = tid - 256; i < 64 * D / 2; i += 128) {      // <S, R>: both tiles have the same layout
+            for (int i = tid - 256; i < 64 * D / 2; i += 128) {      // <S, R>: the tiles have the same layout
                 const uint32_t x = reinterpret_cast<const uint32_t *>(sm + L::oS)[i];
+                const uint32_t z = reinterpret_cast<const uint32_t *>(sm + L::oS + L::kKey)[i];
                 const uint32_t y = reinterpret_cast<const uint32_t *>(sm + L::oR)[i];
-                in = fmaf(low(x), low(y), fmaf(high(x), high(y), in));
+                in = fmaf(low(x) + low(z), low(y), fmaf(high(x) + high(z), high(y), in));
             }
             for (int i = tid - 256; i < C * 8; i += 128) {           // dV = beta X
                 const int r = i / 8, cc = v0 + i % 8 * 8;

@@ -271,11 +271,11 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kern
 // that the chain leaves in shared memory.  kCkpt and kBack: the stores; kBack also the products of dO with P and Q, which
 // the chain adds.  Four loader warps copy chunk c + kStages - 1 while chunk c is worked on.
 //
-// kCkpt (for the backward): no O; writes S before each chunk (bf16, [dv, d]) and W = U / beta, with |beta| held to at
+// kCkpt (for the backward): no O; writes S before each chunk (two bf16 terms, [dv, d]) and W = U / beta, with |beta| held to at
 // least 2^-64 (a beta of 0 then adds 2^-64 W to the state, nothing in fp32).
 // kBack: the reverse recurrence, with the state R = dL/dS [d, dv] after the chunk:
 //   dU = P^T dO + diag(f) K R,  X = T^T dU,  R <- e^{G_C} R + (scale diag(e^G) Q)^T dO - (diag(e^G beta) K)^T X,
-// the same chain with the triangles transposed; writes R after each chunk and X.
+// the same chain with the triangles transposed; writes R after each chunk (bf16) and X.
 //
 // Bound by the chain: mma.sync issues one m16n8k16 each 8.0 cycles on each of the SM's four tensor units (measured,
 // 1 to 16 warps; latency 21), and the products of a chunk depend on one another.  tcgen05 has four times that rate,
@@ -295,7 +295,7 @@ struct ChainArgs {
     float *state_out;                  // kBack: dL/dS before the first
     void *out;                         // kFwd
     __nv_bfloat16 *rows;               // kCkpt: W, kBack: X, as two bf16 terms [2, G, N, dv]
-    __nv_bfloat16 *states;             // kCkpt: S before, kBack: R after each chunk, [G, nc, dv, d]
+    __nv_bfloat16 *states;             // kCkpt: S before each chunk, [2, G, nc, dv, d]; kBack: R after each, [G, nc, dv, d]
 };
 
 template <int D, int NT, int SL, int MODE>
@@ -303,8 +303,8 @@ struct ChainSmem {
     static constexpr int KS = 4 / SL;
     static constexpr int kRow = 2 * D, kKey = C * kRow, kValRow = 32 * SL, kVal = C * kValRow;
     static constexpr int oQ = kKey, oV = 2 * kKey, oW = oV + kVal, kStage = oW + Chunk<NT>::bytes;
-    // of one slice: partial sums; R's terms, then U (float4 [8 tiles][32 lanes]); the state in bf16; kBack: P^T dO and Q^T dO
-    static constexpr int kSum = KS > 1 ? KS * 4096 : 0, kRows = KS > 1 && NT > 2 ? 6144 : 4096, kState = 32 * D;
+    // of one slice: partial sums; R's terms, then U (float4 [8 tiles][32 lanes]); the state in kHeld bf16 terms; kBack: P^T dO and Q^T dO
+    static constexpr int kSum = KS > 1 ? KS * 4096 : 0, kRows = KS > 1 && NT > 2 ? 6144 : 4096, kHeld = MODE == kCkpt ? 2 : 1, kState = kHeld * 32 * D;
     static constexpr int kZ = MODE == kBack ? 4096 + 64 * D : 0;
     static constexpr int oRows = kSum, oState = oRows + kRows, oZ = oState + kState, kSlice = oZ + kZ;
     static constexpr int kStages = 3 * kStage + SL * kSlice <= 227 * 1024 ? 3 : 2;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
     char *mine = sm + L::oSlice + slice * L::kSlice;
     float4 *sums = reinterpret_cast<float4 *>(mine);                                // [KS][8 tiles][32 lanes]
     char *rows = mine + L::oRows;                                                   // R's terms; then U, [8 tiles][32 lanes]
-    uint4 *held = reinterpret_cast<uint4 *>(mine + L::oState);                      // the state: [D / 16][32 lanes]
+    uint4 *held = reinterpret_cast<uint4 *>(mine + L::oState);                      // the state: [kHeld][D / 16][32 lanes]
     float4 *zp = reinterpret_cast<float4 *>(mine + L::oZ), *zq = zp + 8 * 32;       // kBack
     const int q0 = 2 * (lane & 3), br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;   // B operand: row, piece
     const int col = c0 + 16 * slice + (lane >> 2);
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             const uint32_t qt = smem_u32(st) + L::oQ, vt = smem_u32(st) + L::oV, pt = smem_u32(st) + L::oW + W::oP;
             const Vec &vec = *reinterpret_cast<const Vec *>(st + L::oW + W::oVec);
             float x[OWN][4];
-            uint4 was[DK / 16];
+            uint4 was[L::kHeld][DK / 16];
             zero(x);
             if (MODE == kFwd) {
                 // O = scale e^G Q S, then + P U
@@ -547,7 +547,9 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
                     for (int n = 0; n < DK / 8; ++n) zq[(rank * DK / 8 + n) * 32 + lane] = as4(y[n]);
                 }
 #pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks) was[ks] = held[(rank * DK / 16 + ks) * 32 + lane];
+                for (int t = 0; t < L::kHeld; ++t)
+#pragma unroll
+                    for (int ks = 0; ks < DK / 16; ++ks) was[t][ks] = held[(t * D / 16 + rank * DK / 16 + ks) * 32 + lane];
             }
             bar<kPair>(kBarU + slice);                   // U is there; the chain may change `held`
             if (MODE == kFwd) {
@@ -570,13 +572,16 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             } else {
                 // the state as it was held: [dv, d] in bf16
 #pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks) {
-                    const uint32_t s2[4] = {was[ks].x, was[ks].y, was[ks].z, was[ks].w};
+                for (int t = 0; t < L::kHeld; ++t) {
+                    __nv_bfloat16 *to = a.states + (((size_t)t * p.B * p.H + bh) * a.nc + c) * p.dv * p.d;
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const int r = rank * DK + 16 * ks + 8 * (m >> 1) + q0, cc = col + 8 * (m & 1);
-                        if (r < p.d && cc < p.dv)
-                            *reinterpret_cast<uint32_t *>(a.states + (((size_t)bh * a.nc + c) * p.dv + cc) * p.d + r) = s2[m];
+                    for (int ks = 0; ks < DK / 16; ++ks) {
+                        const uint32_t s2[4] = {was[t][ks].x, was[t][ks].y, was[t][ks].z, was[t][ks].w};
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const int r = rank * DK + 16 * ks + 8 * (m >> 1) + q0, cc = col + 8 * (m & 1);
+                            if (r < p.d && cc < p.dv) *reinterpret_cast<uint32_t *>(to + (size_t)cc * p.d + r) = s2[m];
+                        }
                     }
                 }
                 // W = U / beta (X as it is) in two terms
@@ -614,10 +619,13 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
         }
     auto hold = [&] {
 #pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks)
-            held[(k0 / 16 + ks) * 32 + lane] = make_uint4(pack(S[2 * ks][0], S[2 * ks][1]), pack(S[2 * ks][2], S[2 * ks][3]),
-                                                          pack(S[2 * ks + 1][0], S[2 * ks + 1][1]),
-                                                          pack(S[2 * ks + 1][2], S[2 * ks + 1][3]));
+        for (int ks = 0; ks < DK / 16; ++ks) {
+            uint32_t f[L::kHeld][4];
+            split_a<L::kHeld>(S[2 * ks], S[2 * ks + 1], f);
+#pragma unroll
+            for (int t = 0; t < L::kHeld; ++t)
+                held[(t * D / 16 + k0 / 16 + ks) * 32 + lane] = make_uint4(f[t][0], f[t][1], f[t][2], f[t][3]);
+        }
     };
     auto meet = [&] { if (KS > 1) bar<32 * KS>(kBarSlice + slice); };
     hold();
@@ -837,7 +845,7 @@ BackLayout back_layout(const DeltaProblem &p) {
     L.chunks = take(delta_tc_workspace(p));
     L.w = take(rows * p.dv * 4);
     L.x = take(rows * p.dv * 4);
-    L.s0 = take(states * 2);
+    L.s0 = take(states * 4);
     L.ds = take(states * 2);
     L.dq = p.H != p.Hk ? take(rows * p.d * 4) : 0;
     L.dk = p.H != p.Hk ? take(rows * p.d * 4) : 0;
