@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
     char *mine = sm + L::oSlice + slice * L::kSlice;
     float4 *sums = reinterpret_cast<float4 *>(mine);                                // [KS][8 tiles][32 lanes]
     char *rows = mine + L::oRows;                                                   // R's terms; then U, [8 tiles][32 lanes]
-    uint4 *held = reinterpret_cast<uint4 *>(mine + L::oState);                      // the state: [kHeld][D / 16][32 lanes]
+    const uint32_t held = smem_u32(mine + L::oState);                               // the state: [kHeld][16 columns][D]
     float4 *zp = reinterpret_cast<float4 *>(mine + L::oZ), *zq = zp + 8 * 32;       // kBack
     const int q0 = 2 * (lane & 3), br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;   // B operand: row, piece
     const int col = c0 + 16 * slice + (lane >> 2);
@@ -508,8 +508,8 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
                 // O = scale e^G Q S, then + P U
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint4 s4 = held[ks * 32 + lane];
-                    const uint32_t fs[4] = {s4.x, s4.y, s4.z, s4.w};
+                    uint32_t fs[4];
+                    ldsm(fs, held + at<2 * D>(lane & 15, 2 * ks + (lane >> 4)));
 #pragma unroll
                     for (int j = 0; j < OWN; j += 2) {
                         uint32_t fq[4];
@@ -549,7 +549,11 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
 #pragma unroll
                 for (int t = 0; t < L::kHeld; ++t)
 #pragma unroll
-                    for (int ks = 0; ks < DK / 16; ++ks) was[t][ks] = held[(t * D / 16 + rank * DK / 16 + ks) * 32 + lane];
+                    for (int i = 0; i < DK / 16; ++i) {
+                        const int e = 32 * i + lane;     // 16 rows of DK / 8 pieces
+                        was[t][i] = *reinterpret_cast<const uint4 *>(
+                            mine + L::oState + t * 32 * D + at<2 * D>(e / (DK / 8), rank * DK / 8 + e % (DK / 8)));
+                    }
             }
             bar<kPair>(kBarU + slice);                   // U is there; the chain may change `held`
             if (MODE == kFwd) {
@@ -575,13 +579,9 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
                 for (int t = 0; t < L::kHeld; ++t) {
                     __nv_bfloat16 *to = a.states + (((size_t)t * p.B * p.H + bh) * a.nc + c) * p.dv * p.d;
 #pragma unroll
-                    for (int ks = 0; ks < DK / 16; ++ks) {
-                        const uint32_t s2[4] = {was[t][ks].x, was[t][ks].y, was[t][ks].z, was[t][ks].w};
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const int r = rank * DK + 16 * ks + 8 * (m >> 1) + q0, cc = col + 8 * (m & 1);
-                            if (r < p.d && cc < p.dv) *reinterpret_cast<uint32_t *>(to + (size_t)cc * p.d + r) = s2[m];
-                        }
+                    for (int i = 0; i < DK / 16; ++i) {
+                        const int e = 32 * i + lane, cc = c0 + 16 * slice + e / (DK / 8), r = rank * DK + e % (DK / 8) * 8;
+                        if (r < p.d && cc < p.dv) *reinterpret_cast<uint4 *>(to + (size_t)cc * p.d + r) = was[t][i];
                     }
                 }
                 // W = U / beta (X as it is) in two terms
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             split_a<L::kHeld>(S[2 * ks], S[2 * ks + 1], f);
 #pragma unroll
             for (int t = 0; t < L::kHeld; ++t)
-                held[(t * D / 16 + k0 / 16 + ks) * 32 + lane] = make_uint4(f[t][0], f[t][1], f[t][2], f[t][3]);
+                stsm(held + t * 32 * D + at<2 * D>(lane & 15, k0 / 8 + 2 * ks + (lane >> 4)), f[t]);
         }
     };
     auto meet = [&] { if (KS > 1) bar<32 * KS>(kBarSlice + slice); };
