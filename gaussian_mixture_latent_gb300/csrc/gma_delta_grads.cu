@@ -45,7 +45,7 @@ struct Smem {
     static constexpr int oE = oR + kKey;                 // E1 and E2, two terms each, as packed triangles
     static constexpr int oVec = oE + 4 * kTriBytes, oRed = oVec + (int)sizeof(Vec);
     static constexpr int kPitch = D + 8;                 // floats: the exchange of dK's halves, over the slab's tiles
-    static_assert(C * kPitch * 4 <= oE - oDo, "the exchange fits");
+    static_assert(C * kPitch * 4 + 2 * kKey <= oE - oDo, "the exchange, and dQ and dK in bf16, fit");
     // a's three parts and b [64] each, dbeta [64], inner [4]
     static constexpr int kRed = 5 * 64 + 4, total = oRed + kRed * 4;
 };
@@ -336,20 +336,32 @@ __global__ void __launch_bounds__(kThreads, ONE && D == 64 ? 2 : 1) delta_grads_
     }
     dots(sums + 64 * role);
     float *half = reinterpret_cast<float *>(sm + L::oDo);            // the slabs are done with
-    // rows i0 and i1 of dQ or dK
+    // the warp's sixteen rows of dQ or dK: bf16 by way of shared memory, as whole rows; or fp32 as they are
     auto store_rows = [&](__nv_bfloat16 *out, float *heads) {
-        const size_t o0 = (vrow + i0) * p.d + q0, o1 = o0 + (size_t)8 * p.d;
-        const bool in0 = i0 < n_all, in1 = i1 < n_all;
+        if (heads) {
+            const size_t o0 = (vrow + i0) * p.d + q0, o1 = o0 + (size_t)8 * p.d;
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t) {
-            if (8 * t + q0 >= p.d) continue;
-            if (heads) {
-                if (in0) *reinterpret_cast<float2 *>(heads + o0 + 8 * t) = make_float2(acc[t][0], acc[t][1]);
-                if (in1) *reinterpret_cast<float2 *>(heads + o1 + 8 * t) = make_float2(acc[t][2], acc[t][3]);
-            } else {
-                if (in0) *reinterpret_cast<uint32_t *>(out + o0 + 8 * t) = pack(acc[t][0], acc[t][1]);
-                if (in1) *reinterpret_cast<uint32_t *>(out + o1 + 8 * t) = pack(acc[t][2], acc[t][3]);
+            for (int t = 0; t < D / 8; ++t) {
+                if (8 * t + q0 >= p.d) continue;
+                if (i0 < n_all) *reinterpret_cast<float2 *>(heads + o0 + 8 * t) = make_float2(acc[t][0], acc[t][1]);
+                if (i1 < n_all) *reinterpret_cast<float2 *>(heads + o1 + 8 * t) = make_float2(acc[t][2], acc[t][3]);
             }
+            return;
+        }
+        char *mine = sm + L::oDo + C * L::kPitch * 4 + (role * 4 + rb) * 16 * L::kRow;
+#pragma unroll
+        for (int t = 0; t < D / 8; t += 2) {
+            const uint32_t x[4] = {pack(acc[t][0], acc[t][1]), pack(acc[t][2], acc[t][3]), pack(acc[t + 1][0], acc[t + 1][1]),
+                                   pack(acc[t + 1][2], acc[t + 1][3])};
+            stsm(smem_u32(mine + at<L::kRow>(lane & 15, t + (lane >> 4))), x);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const int e = 32 * i + lane, r = e / (D / 8), cc = e % (D / 8);
+            if (rb * 16 + r < n_all && cc * 8 < p.d)
+                *reinterpret_cast<uint4 *>(out + (vrow + rb * 16 + r) * p.d + cc * 8) =
+                    *reinterpret_cast<const uint4 *>(mine + at<L::kRow>(r, cc));
         }
     };
     if (role == 0) {

@@ -160,15 +160,20 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kern
         if (inv) {
             *reinterpret_cast<float2 *>(A + i0 * kFp + j) = make_float2(x[n][0], x[n][1]);
             *reinterpret_cast<float2 *>(A + i1 * kFp + j) = make_float2(x[n][2], x[n][3]);
-        } else {
-            uint32_t t[2];
-            const uint32_t o = tri(rb, n / 2) + 4 * (lane & 3);
-            split<2>(x[n][0], x[n][1], t);
-            *reinterpret_cast<uint32_t *>(P + o + at<32>(r0, n & 1)) = t[0];
-            *reinterpret_cast<uint32_t *>(P + o + at<32>(r0, n & 1) + kTriBytes) = t[1];
-            split<2>(x[n][2], x[n][3], t);
-            *reinterpret_cast<uint32_t *>(P + o + at<32>(r0 + 8, n & 1)) = t[0];
-            *reinterpret_cast<uint32_t *>(P + o + at<32>(r0 + 8, n & 1) + kTriBytes) = t[1];
+        } else if (n % 2) {
+            // a block of P in two terms, as whole rows by way of a corner of I that is not in use yet
+            uint32_t t[2][4];
+            split_a<2>(x[n - 1], x[n], t);
+            char *corner = reinterpret_cast<char *>(I + 32 + 8 * pw);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                stsm(smem_u32(corner + (16 * k + (lane & 15)) * kFp * 4 + (lane >> 4) * 16), t[k]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<uint4 *>(P + k * kTriBytes + tri(rb, n / 2) + at<32>(lane >> 1, lane & 1)) =
+                    *reinterpret_cast<const uint4 *>(corner + (16 * k + (lane >> 1)) * kFp * 4 + (lane & 1) * 16);
+            __syncwarp();
         }
     }
     if (inv) {
@@ -243,16 +248,20 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kern
         *reinterpret_cast<float2 *>(to + 8 * kFp) = make_float2(-z[2], -z[3]);
     }
     __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 10 * 128 / kPrepThreads; ++u) {  // pairs of the ten blocks
-        const int e = pt + u * kPrepThreads, blk = e >> 7, r = (e >> 3) & 15, pc = e & 7;
+    for (int e = pt; e < 10 * 32; e += kPrepThreads) {   // T's terms: the ten blocks in pieces of eight
+        const int blk = e >> 5, r = (e >> 1) & 15, half = e & 1;
         const int ib = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, jb = blk - ib * (ib + 1) / 2;
-        const float2 y = *reinterpret_cast<const float2 *>(I + (16 * ib + r) * kFp + 16 * jb + 2 * pc);
-        uint32_t t[NT];
-        split<NT>(y.x, y.y, t);
+        const float4 *from = reinterpret_cast<const float4 *>(I + (16 * ib + r) * kFp + 16 * jb + 8 * half);
+        const float4 y = from[0], z = from[1];
+        uint32_t t[4][NT];
+        split<NT>(y.x, y.y, t[0]);
+        split<NT>(y.z, y.w, t[1]);
+        split<NT>(z.x, z.y, t[2]);
+        split<NT>(z.z, z.w, t[3]);
 #pragma unroll
         for (int k = 0; k < NT; ++k)
-            *reinterpret_cast<uint32_t *>(to_ws + k * kTriBytes + blk * 512 + at<32>(r, pc >> 2) + 4 * (pc & 3)) = t[k];
+            *reinterpret_cast<uint4 *>(to_ws + k * kTriBytes + blk * 512 + at<32>(r, half)) =
+                make_uint4(t[0][k], t[1][k], t[2][k], t[3][k]);
     }
 }
 
