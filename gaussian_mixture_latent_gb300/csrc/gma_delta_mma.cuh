@@ -98,6 +98,24 @@ __device__ __forceinline__ uint32_t at(int r, int c) {
     return r * ROWB + ((c ^ ((r / per) & mask)) << 4);
 }
 
+// 64 rows of a bf16 matrix (rows of `stride` elements at src) into a tile of ROWB-byte rows, by THREADS threads: zeros in the
+// rows from `rows` and the columns from `cols` on.  A thread stays in one piece column and steps by whole groups of eight
+// rows, so that its place in the tile is computed once.
+template <int ROWB, int THREADS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16 *src, int stride, int rows, int cols, int tid) {
+    constexpr int kPieces = ROWB / 16, kStep = THREADS / kPieces;
+    static_assert(THREADS % kPieces == 0 && kStep % 8 == 0, "whole groups of eight rows");
+    const int r0 = tid / kPieces, c = tid % kPieces;
+    const int n = c * 8 < cols ? rows : 0;
+    const __nv_bfloat16 *from = src + (size_t)r0 * stride + c * 8;
+    dst += at<ROWB>(r0, c);
+#pragma unroll
+    for (int i = 0; i < (64 + kStep - 1) / kStep; ++i) {
+        const int r = r0 + i * kStep;
+        if (64 % kStep == 0 || r < 64) copy16(dst + i * kStep * ROWB, r < n ? from + (size_t)i * kStep * stride : src, r < n);
+    }
+}
+
 // A lower triangular 64 x 64 matrix in bf16 as its ten 16 x 16 blocks of 512 bytes.
 constexpr int kTriBytes = 10 * 512;
 __device__ __forceinline__ uint32_t tri(int ib, int jb) { return (ib * (ib + 1) / 2 + jb) * 512; }

@@ -64,13 +64,8 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kern
     const size_t vrow = (size_t)bh * p.N, krow = ((size_t)b * p.Hk + hk) * p.N;
     char *to_ws = a.chunks + (size_t)blockIdx.x * W::bytes;
     const __nv_bfloat16 *K = static_cast<const __nv_bfloat16 *>(p.Kx), *Q = static_cast<const __nv_bfloat16 *>(p.Qx);
-    for (int i = pt; i < C * (D / 8); i += kPrepThreads) {
-        const int r = i / (D / 8), col = i % (D / 8), row = c * C + r;
-        const bool ok = row < len && col * 8 < p.d;
-        const size_t off = ok ? (krow + row) * p.d + col * 8 : 0;
-        copy16(sb + at<kRow>(r, col), K + off, ok);
-        copy16(sb + L::oQ + at<kRow>(r, col), Q + off, ok);
-    }
+    load_tile<kRow, kPrepThreads>(sb, K + (krow + c * C) * p.d, p.d, len - c * C, p.d, pt);
+    load_tile<kRow, kPrepThreads>(sb + L::oQ, Q + (krow + c * C) * p.d, p.d, len - c * C, p.d, pt);
     copy_commit();
     float *A = reinterpret_cast<float *>(sm + L::oA), *I = reinterpret_cast<float *>(sm + L::oI);
     Vec &vec = *reinterpret_cast<Vec *>(sm + L::oVec);
@@ -439,19 +434,9 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             if (i_th < nc) {
                 const int c = chunk_of(i_th);
                 const uint32_t st = sb + (i_th % L::kStages) * L::kStage;
-                for (int i = lt; i < C * (D / 8); i += kGroup) {
-                    const int r = i / (D / 8), col = i % (D / 8), row = c * C + r;
-                    const bool ok = row < len && col * 8 < p.d;
-                    const size_t off = ok ? (krow + row) * p.d + col * 8 : 0;
-                    copy16(st + at<L::kRow>(r, col), K + off, ok);
-                    if (MODE != kCkpt) copy16(st + L::oQ + at<L::kRow>(r, col), Q + off, ok);
-                }
-                for (int i = lt; i < C * 2 * SL; i += kGroup) {
-                    const int r = i / (2 * SL), col = i % (2 * SL), row = c * C + r;
-                    const bool ok = row < len && c0 + col * 8 < p.dv;
-                    const size_t off = ok ? (vrow + row) * p.dv + c0 + col * 8 : 0;
-                    copy16(st + L::oV + at<L::kValRow>(r, col), V + off, ok);
-                }
+                load_tile<L::kRow, kGroup>(st, K + (krow + c * C) * p.d, p.d, len - c * C, p.d, lt);
+                if (MODE != kCkpt) load_tile<L::kRow, kGroup>(st + L::oQ, Q + (krow + c * C) * p.d, p.d, len - c * C, p.d, lt);
+                load_tile<L::kValRow, kGroup>(st + L::oV, V + (vrow + c * C) * p.dv + c0, p.dv, len - c * C, p.dv - c0, lt);
                 const char *ws = a.chunks + ((size_t)bh * a.nc + c) * W::bytes;
                 for (int i = lt; i < W::bytes / 16; i += kGroup) copy16(st + L::oW + 16 * i, ws + 16 * i, true);
             }
