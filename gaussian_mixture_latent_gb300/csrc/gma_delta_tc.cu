@@ -27,8 +27,9 @@ constexpr int C = kTcRows;
 // -------------------------------------------------------------------------------------------------- delta_prep
 // One CTA of eight warps to a chunk.  Warps 0-3 take a row block of K K^T each and the inverse, warps 4-7 Q K^T.
 // T is inverted in fp32: 16 x 16 diagonal blocks by substitution (a product of powers would overflow for repeated
-// keys), joined to 32 and 64 by X21 = -T22 (A21 T11) with products of NT terms.  Bound by the latency of that chain of small
-// steps: three CTAs share an SM.
+// keys), joined to 32 and 64 by X21 = -T22 (A21 T11) with products of NT terms.  Bound by issue slots and the latency of
+// that chain of small steps: three or four CTAs share an SM (148 us for the 12288 chunks of 96 heads x 8192 rows of 64 x 64,
+// 3.2 TB/s; 58 % of the issue slots; two CTAs an SM took 210 us).
 constexpr int kPrepThreads = 256;
 enum { kBarInv = 1, kBarPair = 2 };    // named barriers; the pairs use 2..5
 
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kern
 // the same chain with the triangles transposed; writes R after each chunk (bf16) and X.
 //
 // Bound by the chain: mma.sync issues one m16n8k16 each 8.0 cycles on each of the SM's four tensor units (measured,
-// 1 to 16 warps; latency 21), and the products of a chunk depend on one another.  tcgen05 has four times that rate,
+// 1 to 16 warps; latency 21), and the products of a chunk depend on one another.  64 x 64, SL = 4: 280 products of 8
+// cycles on each unit, 2240 of the 4000 cycles that a chunk takes (269 us for 96 heads x 8192 rows).  tcgen05 has four times that rate,
 // but its accumulators are in TMEM: three dependent products a chunk would each pay a round trip (load, split, store,
 // fence, issue) of about a chunk's time here.
 enum Mode { kFwd, kCkpt, kBack };
@@ -794,7 +796,9 @@ cudaError_t chain(ChainArgs a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// One CTA to an SM, four chain warps to a CTA: as many of them to 16 columns as one wave of CTAs allows.
+// One CTA to an SM, four chain warps to a CTA: as many of them to 16 columns as one wave of CTAs allows.  Measured over
+// 2048 rows, for SL = 1, 2, 4 (us):  64 x 64, 38 heads 47, 60, 77;  64 heads 88, 60, 77;  96 heads 128, 112, 78;
+// 128 x 128 with the state, 19 heads 68, 92, 131;  32 heads 129, 95, 134;  64 heads 252, 182, 135;  152 heads 504, 359, 266.
 template <int D, int NT, int MODE>
 cudaError_t chains(const ChainArgs &a, cudaStream_t s) {
     const long long heads = (long long)a.p.B * a.p.H;
