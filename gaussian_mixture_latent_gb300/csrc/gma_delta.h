@@ -25,7 +25,7 @@ struct DeltaRec {
     float *state_out;                 // the same layout, or null; may equal state_in
     const int *slots;                 // [B] pool index of each batch entry, or null (entry b at b)
     int n_states;
-    void *out;                        // forward: O; backward: dV (types of V)
+    void *out;                        // forward: O, or null; backward: dV (types of V)
     float *rows_out;                  // forward: w [G, N, dv]; backward: dU [G, N, dv]; or null
     float *ckpt;                      // [G, ceil(N / kRecChunk), d, dv]: S before / dS after each chunk; or null
 };
@@ -35,8 +35,10 @@ constexpr int kStepRows = 8;
 cudaError_t delta_step(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s);
 // Any number of rows; no slots.
 cudaError_t delta_rec_forward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s);
-// p.V is dO; state_in is dL/dS after the last row, state_out dL/dS before the first
-cudaError_t delta_rec_backward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s);
+// Both recurrences of the backward.  back: V is dO, state_in is dL/dS after the last row, state_out dL/dS before the first;
+// ckpt: the forward's, for w and the checkpoints (its out may be null).
+cudaError_t delta_rec_backward(const DeltaProblem &pb, const DeltaRec &back, const DeltaProblem &pc, const DeltaRec &ckpt,
+                               cudaStream_t s);
 
 // ----- chunks of 64 rows on the tensor cores, bf16: gma_delta_tc.cu -----
 constexpr int kTcRows = 64;

@@ -168,16 +168,10 @@ gma_status gma_delta_backward(const gma_delta_desc *desc, const void *Qx, const 
         return launched(delta_tc_backward(p, state_in, dO, dstate_out, dQx, dKx, dV, dg, dbeta, dstate_in,
                                           ws + kHeaderBytes, s));
     const RecLayout L = backward_layout(desc);
-    cudaError_t e;
-    if (desc->N > 0) {
-        // the states before each chunk and w of each row; its O goes where dV will be written
-        DeltaRec f{};
-        f.state_in = state_in;
-        f.out = dV;
-        f.rows_out = at(L.w);
-        f.ckpt = at(L.s0);
-        if ((e = delta_rec_forward(p, f, s)) != cudaSuccess) return launched(e);
-    }
+    DeltaRec f{};                                        // the states before each chunk and w of each row
+    f.state_in = state_in;
+    f.rows_out = at(L.w);
+    f.ckpt = at(L.s0);
     DeltaProblem pb = p;
     pb.V = dO;
     DeltaRec r{};
@@ -186,7 +180,8 @@ gma_status gma_delta_backward(const gma_delta_desc *desc, const void *Qx, const 
     r.out = dV;
     r.rows_out = at(L.du);
     r.ckpt = at(L.ds);
-    if ((e = delta_rec_backward(pb, r, s)) != cudaSuccess) return launched(e);
+    cudaError_t e = delta_rec_backward(pb, r, p, f, s);
+    if (e != cudaSuccess) return launched(e);
     if (desc->N == 0) return GMA_OK;
     const bool shared = desc->H != desc->Hk;
     const DeltaGrads ga{dO, at(L.w), at(L.du), at(L.s0), at(L.ds), shared ? at(L.dq) : nullptr,

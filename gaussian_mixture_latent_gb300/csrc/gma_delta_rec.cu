@@ -236,14 +236,14 @@ constexpr int kSeqThreads = 32 * (kSeqWarps + kSeqLoaders);
 
 // R4: float4s of the state's column in a lane; lane (8 row groups, 4 columns) has rows 32 i + 4 (lane / 4) + 0..3.
 template <typename In, int R4, bool BWD>
-__global__ void __launch_bounds__(kSeqThreads) delta_seq_kernel(const RecArgs a) {
+__device__ __forceinline__ void seq_cta(const RecArgs &a, const int block) {
     constexpr int kD = 32 * R4, kPitch = 2 * kD + kSeqCols;
     extern __shared__ __align__(16) float sm[];          // [2][kSeqRows][q | k | v]
     __shared__ float4 s_row[2][kSeqRows];                // decay, beta, q.k
     const DeltaProblem &p = a.p;
     const int d = p.d, dv = p.dv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int slice = blockIdx.x % a.slices;
-    const int bh = blockIdx.x / a.slices, b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
+    const int slice = block % a.slices;
+    const int bh = block / a.slices, b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
     const int len = delta_len(p.lengths, b, p.N), blocks = (len + kSeqRows - 1) / kSeqRows;
     const size_t head_rows = (size_t)bh * p.N, key_rows = ((size_t)b * p.Hk + hk) * p.N;
     In *out = static_cast<In *>(a.r.out);
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kSeqThreads) delta_seq_kernel(const RecArgs a)
         }
         // rows that do not exist are written as zeros
         const int w = min(kSeqCols, dv - slice * kSeqCols);
-        for (size_t i = tid - 32 * kSeqWarps; i < (size_t)(p.N - len) * w; i += 32 * kSeqLoaders)
+        for (size_t i = tid - 32 * kSeqWarps; out && i < (size_t)(p.N - len) * w; i += 32 * kSeqLoaders)
             delta_out(out, (head_rows + len + i / w) * dv + slice * kSeqCols + (int)(i % w), 0.f);
         return;
     }
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kSeqThreads) delta_seq_kernel(const RecArgs a)
             }
             if ((t % 8 == 7 || t == n - 1) && lr <= t % 8 && c < dv) {       // eight rows' results at a time
                 const size_t at = (head_rows + row_of(blk * kSeqRows + t / 8 * 8 + lr)) * dv + c;
-                delta_out(out, at, keep_o);
+                if (out) delta_out(out, at, keep_o);
                 if (a.r.rows_out) a.r.rows_out[at] = keep_y;
             }
         }
@@ -369,12 +369,37 @@ __global__ void __launch_bounds__(kSeqThreads) delta_seq_kernel(const RecArgs a)
 }
 
 template <typename In, int R4, bool BWD>
+__global__ void __launch_bounds__(kSeqThreads) delta_seq_kernel(const RecArgs a) {
+    seq_cta<In, R4, BWD>(a, blockIdx.x);
+}
+
+// The two recurrences of the backward, which do not depend on one another, side by side.
+template <typename In, int R4>
+__global__ void __launch_bounds__(kSeqThreads) delta_seqs_kernel(const RecArgs back, const RecArgs ckpt) {
+    const int n = gridDim.x / 2;
+    if (blockIdx.x < n) seq_cta<In, R4, true>(back, blockIdx.x);
+    else seq_cta<In, R4, false>(ckpt, blockIdx.x - n);
+}
+
+constexpr int seq_smem(int r4) { return 2 * kSeqRows * (64 * r4 + kSeqCols) * (int)sizeof(float); }
+
+template <typename In, int R4, bool BWD>
 cudaError_t launch_seq(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
     const RecArgs a{p, r, (p.dv + kSeqCols - 1) / kSeqCols, 0, 0};
-    constexpr int smem = 2 * kSeqRows * (64 * R4 + kSeqCols) * (int)sizeof(float);
-    const cudaError_t e = set_dyn_smem((const void *)delta_seq_kernel<In, R4, BWD>, smem);
+    const cudaError_t e = set_dyn_smem((const void *)delta_seq_kernel<In, R4, BWD>, seq_smem(R4));
     if (e != cudaSuccess) return e;
-    delta_seq_kernel<In, R4, BWD><<<(unsigned)((size_t)p.B * p.H * a.slices), kSeqThreads, smem, s>>>(a);
+    delta_seq_kernel<In, R4, BWD><<<(unsigned)((size_t)p.B * p.H * a.slices), kSeqThreads, seq_smem(R4), s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename In, int R4>
+cudaError_t launch_seqs(const DeltaProblem &pb, const DeltaRec &back, const DeltaProblem &pc, const DeltaRec &ckpt,
+                        cudaStream_t s) {
+    const int slices = (pb.dv + kSeqCols - 1) / kSeqCols;
+    const cudaError_t e = set_dyn_smem((const void *)delta_seqs_kernel<In, R4>, seq_smem(R4));
+    if (e != cudaSuccess) return e;
+    delta_seqs_kernel<In, R4><<<(unsigned)(2 * (size_t)pb.B * pb.H * slices), kSeqThreads, seq_smem(R4), s>>>(
+        RecArgs{pb, back, slices, 0, 0}, RecArgs{pc, ckpt, slices, 0, 0});
     return cudaGetLastError();
 }
 
@@ -384,6 +409,15 @@ cudaError_t seq_dispatch(const DeltaProblem &p, const DeltaRec &r, cudaStream_t 
     if (p.d <= 64) return launch_seq<In, 2, BWD>(p, r, s);
     if (p.d <= 128) return launch_seq<In, 4, BWD>(p, r, s);
     return launch_seq<In, 8, BWD>(p, r, s);
+}
+
+template <typename In>
+cudaError_t seqs_dispatch(const DeltaProblem &pb, const DeltaRec &back, const DeltaProblem &pc, const DeltaRec &ckpt,
+                          cudaStream_t s) {
+    if (pb.d <= 32) return launch_seqs<In, 1>(pb, back, pc, ckpt, s);
+    if (pb.d <= 64) return launch_seqs<In, 2>(pb, back, pc, ckpt, s);
+    if (pb.d <= 128) return launch_seqs<In, 4>(pb, back, pc, ckpt, s);
+    return launch_seqs<In, 8>(pb, back, pc, ckpt, s);
 }
 
 // ----------------------------------------------------------------------------------------------------------------
@@ -660,8 +694,11 @@ cudaError_t delta_rec_forward(const DeltaProblem &p, const DeltaRec &r, cudaStre
     return p.bf16 ? seq_dispatch<__nv_bfloat16, false>(p, r, s) : seq_dispatch<float, false>(p, r, s);
 }
 
-cudaError_t delta_rec_backward(const DeltaProblem &p, const DeltaRec &r, cudaStream_t s) {
-    return p.bf16 ? seq_dispatch<__nv_bfloat16, true>(p, r, s) : seq_dispatch<float, true>(p, r, s);
+cudaError_t delta_rec_backward(const DeltaProblem &pb, const DeltaRec &back, const DeltaProblem &pc, const DeltaRec &ckpt,
+                               cudaStream_t s) {
+    if (pb.N == 0)                                       // nothing but the state's gradient to hand on
+        return pb.bf16 ? seq_dispatch<__nv_bfloat16, true>(pb, back, s) : seq_dispatch<float, true>(pb, back, s);
+    return pb.bf16 ? seqs_dispatch<__nv_bfloat16>(pb, back, pc, ckpt, s) : seqs_dispatch<float>(pb, back, pc, ckpt, s);
 }
 
 cudaError_t delta_rec_grads(const DeltaProblem &p, const DeltaGrads &a, cudaStream_t s) {

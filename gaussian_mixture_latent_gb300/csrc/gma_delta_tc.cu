@@ -407,7 +407,7 @@ __device__ __forceinline__ void scale_cols(float (&x)[4], float2 f) {
 __device__ __forceinline__ float2 pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 
 template <int D, int NT, int SL, int MODE>
-__global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainArgs a) {
+__device__ __forceinline__ void chain_cta(const ChainArgs &a, const int block) {
     using L = ChainSmem<D, NT, SL, MODE>;
     using W = Chunk<NT>;
     constexpr int KS = L::KS, DK = D / KS, OWN = 8 / KS;
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
     extern __shared__ __align__(128) char sm[];
     const DeltaProblem &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int bh = blockIdx.x / a.groups, grp = blockIdx.x % a.groups;
+    const int bh = block / a.groups, grp = block % a.groups;
     const int b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
     const int len = delta_len(p.lengths, b, p.N);
     const int nc = (len + C - 1) / C;
@@ -777,6 +777,19 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
             }
 }
 
+template <int D, int NT, int SL>
+__global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainArgs a) {
+    chain_cta<D, NT, SL, kFwd>(a, blockIdx.x);
+}
+
+// The two chains of the backward, which do not depend on one another: the reverse one, which takes longer, first.
+template <int D, int NT, int SL>
+__global__ void __launch_bounds__(3 * kGroup, 1) delta_chains_kernel(const ChainArgs back, const ChainArgs ckpt) {
+    const int n = gridDim.x / 2;
+    if (blockIdx.x < n) chain_cta<D, NT, SL, kBack>(back, blockIdx.x);
+    else chain_cta<D, NT, SL, kCkpt>(ckpt, blockIdx.x - n);
+}
+
 template <int D, int NT>
 cudaError_t prep(const DeltaProblem &p, char *chunks, bool held, cudaStream_t s) {
     const PrepArgs a{p, chunks, (p.N + C - 1) / C, held};
@@ -786,25 +799,50 @@ cudaError_t prep(const DeltaProblem &p, char *chunks, bool held, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <int D, int NT, int SL, int MODE>
-cudaError_t chain(ChainArgs a, cudaStream_t s) {
-    using L = ChainSmem<D, NT, SL, MODE>;
-    a.groups = (a.p.dv + 16 * SL - 1) / (16 * SL);
-    const cudaError_t e = set_dyn_smem((const void *)delta_chain_kernel<D, NT, SL, MODE>, L::total);
-    if (e != cudaSuccess) return e;
-    delta_chain_kernel<D, NT, SL, MODE><<<(unsigned)(a.p.B * a.p.H * a.groups), 3 * kGroup, L::total, s>>>(a);
-    return cudaGetLastError();
-}
-
 // One CTA to an SM, four chain warps to a CTA: as many of them to 16 columns as one wave of CTAs allows.  Measured over
 // 2048 rows, for SL = 1, 2, 4 (us):  64 x 64, 38 heads 47, 60, 77;  64 heads 88, 60, 77;  96 heads 128, 112, 78;
 // 128 x 128 with the state, 19 heads 68, 92, 131;  32 heads 129, 95, 134;  64 heads 252, 182, 135;  152 heads 504, 359, 266.
-template <int D, int NT, int MODE>
-cudaError_t chains(const ChainArgs &a, cudaStream_t s) {
-    const long long heads = (long long)a.p.B * a.p.H;
-    if (heads * ((a.p.dv + 15) / 16) <= 152) return chain<D, NT, 1, MODE>(a, s);
-    if (heads * ((a.p.dv + 31) / 32) <= 152) return chain<D, NT, 2, MODE>(a, s);
-    return chain<D, NT, 4, MODE>(a, s);
+int slices(long long heads, int dv) {
+    return heads * ((dv + 15) / 16) <= 152 ? 1 : heads * ((dv + 31) / 32) <= 152 ? 2 : 4;
+}
+
+template <int D, int NT, int SL>
+cudaError_t chain(ChainArgs a, cudaStream_t s) {
+    using L = ChainSmem<D, NT, SL, kFwd>;
+    a.groups = (a.p.dv + 16 * SL - 1) / (16 * SL);
+    const cudaError_t e = set_dyn_smem((const void *)delta_chain_kernel<D, NT, SL>, L::total);
+    if (e != cudaSuccess) return e;
+    delta_chain_kernel<D, NT, SL><<<(unsigned)(a.p.B * a.p.H * a.groups), 3 * kGroup, L::total, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int D, int NT, int SL>
+cudaError_t both_chains(ChainArgs back, ChainArgs ckpt, cudaStream_t s) {
+    constexpr int b = ChainSmem<D, NT, SL, kBack>::total, c = ChainSmem<D, NT, SL, kCkpt>::total, smem = b > c ? b : c;
+    back.groups = ckpt.groups = (back.p.dv + 16 * SL - 1) / (16 * SL);
+    const cudaError_t e = set_dyn_smem((const void *)delta_chains_kernel<D, NT, SL>, smem);
+    if (e != cudaSuccess) return e;
+    delta_chains_kernel<D, NT, SL><<<(unsigned)(2 * back.p.B * back.p.H * back.groups), 3 * kGroup, smem, s>>>(back, ckpt);
+    return cudaGetLastError();
+}
+
+template <int D, int NT>
+cudaError_t forward(const ChainArgs &a, char *chunks, cudaStream_t s) {
+    const cudaError_t e = prep<D, NT>(a.p, chunks, false, s);
+    if (e != cudaSuccess) return e;
+    const int sl = slices((long long)a.p.B * a.p.H, a.p.dv);
+    return sl == 1 ? chain<D, NT, 1>(a, s) : sl == 2 ? chain<D, NT, 2>(a, s) : chain<D, NT, 4>(a, s);
+}
+
+template <int D, int NT>
+cudaError_t backward(const ChainArgs &back, const ChainArgs &ckpt, char *chunks, int &bytes, int &vec_at, cudaStream_t s) {
+    bytes = Chunk<NT>::bytes;
+    vec_at = Chunk<NT>::oVec;
+    const cudaError_t e = prep<D, NT>(ckpt.p, chunks, true, s);
+    if (e != cudaSuccess) return e;
+    const int sl = slices(2LL * back.p.B * back.p.H, back.p.dv);
+    return sl == 1 ? both_chains<D, NT, 1>(back, ckpt, s)
+                   : sl == 2 ? both_chains<D, NT, 2>(back, ckpt, s) : both_chains<D, NT, 4>(back, ckpt, s);
 }
 
 }  // namespace
@@ -820,15 +858,8 @@ size_t delta_tc_workspace(const DeltaProblem &p) {
 cudaError_t delta_tc_forward(const DeltaProblem &p, const float *state_in, void *out, float *state_out, char *ws,
                              cudaStream_t s) {
     const ChainArgs a{p, ws, (p.N + C - 1) / C, 0, state_in, state_out, out, nullptr, nullptr};
-    cudaError_t e = cudaSuccess;
-    auto both = [&](auto d, auto nt) {
-        constexpr int D = decltype(d)::value, NT = decltype(nt)::value;
-        e = prep<D, NT>(p, ws, false, s);
-        if (e == cudaSuccess) e = chains<D, NT, kFwd>(a, s);
-    };
-    if (p.d <= 64) state_out ? both(Int<64>{}, Int<3>{}) : both(Int<64>{}, Int<2>{});
-    else state_out ? both(Int<128>{}, Int<3>{}) : both(Int<128>{}, Int<2>{});
-    return e;
+    if (p.d <= 64) return state_out ? forward<64, 3>(a, ws, s) : forward<64, 2>(a, ws, s);
+    return state_out ? forward<128, 3>(a, ws, s) : forward<128, 2>(a, ws, s);
 }
 
 namespace {
@@ -865,19 +896,11 @@ cudaError_t delta_tc_backward(const DeltaProblem &p, const float *state_in, cons
     ChainArgs r{p, chunks, nc, 0, dstate_out, dstate_in, nullptr, reinterpret_cast<__nv_bfloat16 *>(ws + L.x),
                 reinterpret_cast<__nv_bfloat16 *>(ws + L.ds)};
     r.p.V = dO;
-    cudaError_t e = cudaSuccess;
     int bytes = 0, vec_at = 0;
     // three terms where the state's gradient is returned in fp32, as in the forward
-    auto run = [&](auto d, auto nt) {
-        constexpr int D = decltype(d)::value, NT = decltype(nt)::value;
-        bytes = Chunk<NT>::bytes;
-        vec_at = Chunk<NT>::oVec;
-        e = prep<D, NT>(p, chunks, true, s);
-        if (e == cudaSuccess) e = chains<D, NT, kCkpt>(f, s);
-        if (e == cudaSuccess) e = chains<D, NT, kBack>(r, s);
-    };
-    if (p.d <= 64) dstate_in ? run(Int<64>{}, Int<3>{}) : run(Int<64>{}, Int<2>{});
-    else dstate_in ? run(Int<128>{}, Int<3>{}) : run(Int<128>{}, Int<2>{});
+    cudaError_t e = p.d <= 64 ? dstate_in ? backward<64, 3>(r, f, chunks, bytes, vec_at, s) : backward<64, 2>(r, f, chunks, bytes, vec_at, s)
+                    : dstate_in ? backward<128, 3>(r, f, chunks, bytes, vec_at, s)
+                                : backward<128, 2>(r, f, chunks, bytes, vec_at, s);
     if (e != cudaSuccess) return e;
     const bool shared = p.H != p.Hk;
     float *dq = shared ? reinterpret_cast<float *>(ws + L.dq) : nullptr;
