@@ -15,8 +15,11 @@
 // column sums go over the 8 warps through shared memory.  The time is the state's read and write (256 x 32 heads of
 // 128 x 128, one row: 183 us for 1.08 GB, 5.9 TB/s; an in-place scaling of as much memory takes 156).
 // delta_seq_kernel (longer): a warp holds [d, 4] of the state, eight lanes to a column, and needs no other warp: a row's
-// sums are three shuffles.  Four loader warps stage the next 16 rows (and their decays and q.k) meanwhile.  The time is the
-// latency of one row after another (5 x 6 heads x 1531 rows of 64 x 64: 220 us, 270 cycles a row).
+// sums are three shuffles.  Four loader warps stage the next 32 rows (and their decays and q.k) meanwhile: 5 x 6 heads x
+// 1531 rows of 64 x 64 take 216 us (with 16 rows at a time 8 % more, with eight loader warps none less).  The time is the
+// latency of one row after another, 290 cycles.  With the next row's products against the state put ahead of the update,
+// and the products of neighbouring rows to correct them, the chain is shorter but the loaders do three dots for one:
+// 245 us.
 // The step kernel takes a little more than 1 us a row beside its start (16 heads of 128 x 128: 8.2 us for one row, 15 for
 // eight); the chunks of gma_delta_tc.cu cost 14 us from one row to 64, so that nine rows and more go there.
 #include <cstdint>
@@ -231,7 +234,7 @@ cudaError_t step_dispatch(const DeltaProblem &p, const DeltaRec &r, cudaStream_t
 }
 
 // ----------------------------------------------------------------------------------------------------------------
-constexpr int kSeqWarps = 8, kSeqLoaders = 4, kSeqRows = 16, kSeqCols = 4 * kSeqWarps;
+constexpr int kSeqWarps = 8, kSeqLoaders = 4, kSeqRows = 32, kSeqCols = 4 * kSeqWarps;
 constexpr int kSeqThreads = 32 * (kSeqWarps + kSeqLoaders);
 
 // R4: float4s of the state's column in a lane; lane (8 row groups, 4 columns) has rows 32 i + 4 (lane / 4) + 0..3.
@@ -254,36 +257,40 @@ __device__ __forceinline__ void seq_cta(const RecArgs &a, const int block) {
         const int lw = warp - kSeqWarps, vc = slice * kSeqCols + lane;
         for (int blk = 0; blk <= blocks; ++blk) {
             if (blk < blocks) {
-                constexpr int kEach = kSeqRows / kSeqLoaders;
-                float q[kEach][R4], k[kEach][R4], v[kEach], ga[kEach], be[kEach];
+                constexpr int kEach = R4 <= 4 ? kSeqRows / kSeqLoaders : 4;     // the rows that a warp's registers hold
+                static_assert(kSeqRows % (kEach * kSeqLoaders) == 0, "whole passes");
+#pragma unroll 1
+                for (int t0 = 0; t0 < kSeqRows; t0 += kEach * kSeqLoaders) {
+                    float q[kEach][R4], k[kEach][R4], v[kEach], ga[kEach], be[kEach];
 #pragma unroll
-                for (int m = 0; m < kEach; ++m) {        // every read first, then what is done with them
-                    const int t = blk * kSeqRows + m * kSeqLoaders + lw, row = row_of(t);
-                    const bool in = t < len;
-                    v[m] = in && vc < dv ? delta_in(V, (head_rows + row) * dv + vc) : 0.f;
-                    ga[m] = in ? delta_gate(p.g, head_rows + row, p.gate_bf16) : 0.f;
-                    be[m] = in ? delta_gate(p.beta, head_rows + row, p.gate_bf16) : 0.f;
+                    for (int m = 0; m < kEach; ++m) {    // every read first, then what is done with them
+                        const int t = blk * kSeqRows + t0 + m * kSeqLoaders + lw, row = row_of(t);
+                        const bool in = t < len;
+                        v[m] = in && vc < dv ? delta_in(V, (head_rows + row) * dv + vc) : 0.f;
+                        ga[m] = in ? delta_gate(p.g, head_rows + row, p.gate_bf16) : 0.f;
+                        be[m] = in ? delta_gate(p.beta, head_rows + row, p.gate_bf16) : 0.f;
 #pragma unroll
-                    for (int i = 0; i < R4; ++i) {
-                        const int e = 32 * i + lane;
-                        q[m][i] = in && e < d ? delta_in(Q, (key_rows + row) * d + e) : 0.f;
-                        k[m][i] = in && e < d ? delta_in(K, (key_rows + row) * d + e) : 0.f;
+                        for (int i = 0; i < R4; ++i) {
+                            const int e = 32 * i + lane;
+                            q[m][i] = in && e < d ? delta_in(Q, (key_rows + row) * d + e) : 0.f;
+                            k[m][i] = in && e < d ? delta_in(K, (key_rows + row) * d + e) : 0.f;
+                        }
                     }
-                }
 #pragma unroll
-                for (int m = 0; m < kEach; ++m) {
-                    const int t = m * kSeqLoaders + lw;
-                    float *to = sm + ((blk & 1) * kSeqRows + t) * kPitch;
-                    float x = 0.f;
+                    for (int m = 0; m < kEach; ++m) {
+                        const int t = t0 + m * kSeqLoaders + lw;
+                        float *to = sm + ((blk & 1) * kSeqRows + t) * kPitch;
+                        float x = 0.f;
 #pragma unroll
-                    for (int i = 0; i < R4; ++i) {
-                        to[32 * i + lane] = q[m][i];
-                        to[kD + 32 * i + lane] = k[m][i];
-                        x = fmaf(q[m][i], k[m][i], x);
+                        for (int i = 0; i < R4; ++i) {
+                            to[32 * i + lane] = q[m][i];
+                            to[kD + 32 * i + lane] = k[m][i];
+                            x = fmaf(q[m][i], k[m][i], x);
+                        }
+                        to[2 * kD + lane] = v[m];
+                        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+                        if (lane == 0) s_row[blk & 1][t] = make_float4(expf(ga[m]), be[m], x, 0.f);
                     }
-                    to[2 * kD + lane] = v[m];
-                    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-                    if (lane == 0) s_row[blk & 1][t] = make_float4(expf(ga[m]), be[m], x, 0.f);
                 }
             }
             __syncthreads();
@@ -369,13 +376,13 @@ __device__ __forceinline__ void seq_cta(const RecArgs &a, const int block) {
 }
 
 template <typename In, int R4, bool BWD>
-__global__ void __launch_bounds__(kSeqThreads) delta_seq_kernel(const RecArgs a) {
+__global__ void __launch_bounds__(kSeqThreads, 1) delta_seq_kernel(const RecArgs a) {
     seq_cta<In, R4, BWD>(a, blockIdx.x);
 }
 
 // The two recurrences of the backward, which do not depend on one another, side by side.
 template <typename In, int R4>
-__global__ void __launch_bounds__(kSeqThreads) delta_seqs_kernel(const RecArgs back, const RecArgs ckpt) {
+__global__ void __launch_bounds__(kSeqThreads, 1) delta_seqs_kernel(const RecArgs back, const RecArgs ckpt) {
     const int n = gridDim.x / 2;
     if (blockIdx.x < n) seq_cta<In, R4, true>(back, blockIdx.x);
     else seq_cta<In, R4, false>(ckpt, blockIdx.x - n);
@@ -432,8 +439,9 @@ cudaError_t seqs_dispatch(const DeltaProblem &pb, const DeltaRec &back, const De
 //          + e^{G_C} <S0, R>,   M_ij = D_ij (scale (dO_i.u_j)(q_i.k_j) - (x_i.u_j)(k_i.k_j))
 // The first sum is taken as running sums of (row sums - column sums) of M over the rows i, j; pairs with both rows
 // on one side of t then cancel as the same numbers in fp32.
-constexpr int kGThreads = 256;
+constexpr int kGThreads = 512;
 constexpr int C = kRecChunk;
+constexpr int kGRows = C * 128 / kGThreads;           // rows of the chunk to each of the groups of 128 threads
 
 __host__ __device__ inline int grad_pitch(int n) {       // floats; an odd number of float4s keeps rows on other banks
     const int q = (n + 3) / 4;
@@ -462,8 +470,8 @@ __global__ void __launch_bounds__(kGThreads) delta_rec_grads_kernel(const GradAr
     const int d = p.d, dv = p.dv, pd = grad_pitch(d), pv = grad_pitch(dv), tid = threadIdx.x;
     const int d4 = (d + 3) / 4, v4 = (dv + 3) / 4;
     float *q = sm, *k = q + C * pd, *dO = k + C * pd, *u = dO + C * pv, *x = u + C * pv;
-    float *E1 = x + C * pv, *E2 = E1 + C * (C + 1), *red = E2 + C * (C + 1);   // red: [8 warps][C][2]
-    __shared__ float hi[C], lo[C], beta[C], e0[C], f1[C], rowM[C], colM[C], dbeta[C], inner[8];
+    float *E1 = x + C * pv, *E2 = E1 + C * (C + 1), *red = E2 + C * (C + 1);   // red: [warps][kGRows][2]
+    __shared__ float hi[C], lo[C], beta[C], e0[C], f1[C], rowM[C], colM[C], dbeta[C], inner[kGThreads / 32];
     __shared__ double gsum[C];
     const int nchunk = (p.N + C - 1) / C;
     const int c = blockIdx.x % nchunk, bh = blockIdx.x / nchunk, b = bh / p.H, h = bh % p.H, hk = h / (p.H / p.Hk);
@@ -514,10 +522,11 @@ __global__ void __launch_bounds__(kGThreads) delta_rec_grads_kernel(const GradAr
     }
     __syncthreads();
     // E1 = scale D o (dO U^T), E2 = D o (X U^T) strictly below the diagonal, and M's row and column sums
-    float m[4];
+    constexpr int kEach = C * C / kGThreads, kAcross = kGThreads / C;      // elements of a thread; threads of a row
+    float m[kEach];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int i = tid / 8, j = tid % 8 + 8 * e;
+    for (int e = 0; e < kEach; ++e) {
+        const int i = tid / kAcross, j = tid % kAcross + kAcross * e;
         float a1 = 0.f, a2 = 0.f;
         m[e] = 0.f;
         if (j <= i) {
@@ -534,7 +543,7 @@ __global__ void __launch_bounds__(kGThreads) delta_rec_grads_kernel(const GradAr
     }
     float *M = red;                                      // [C][C + 1], before `red` is used
 #pragma unroll
-    for (int e = 0; e < 4; ++e) M[(tid / 8) * (C + 1) + tid % 8 + 8 * e] = m[e];
+    for (int e = 0; e < kEach; ++e) M[(tid / kAcross) * (C + 1) + tid % kAcross + kAcross * e] = m[e];
     __syncthreads();
     if (tid < C) {
         float s = 0.f;
@@ -547,26 +556,26 @@ __global__ void __launch_bounds__(kGThreads) delta_rec_grads_kernel(const GradAr
     }
     __syncthreads();
     const float *S0 = A.s0 + ((size_t)bh * nchunk + c) * d * dv, *R = A.ds + ((size_t)bh * nchunk + c) * d * dv;
-    const int half = tid / 128, i0 = half * 16, warp = tid / 32, lane = tid % 32;
-    float acc_row[16], acc_key[16], in = 0.f;
+    const int group = tid / 128, i0 = group * kGRows, warp = tid / 32, lane = tid % 32;
+    float acc_row[kGRows], acc_key[kGRows], in = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc_row[i] = acc_key[i] = 0.f;
+    for (int i = 0; i < kGRows; ++i) acc_row[i] = acc_key[i] = 0.f;
     In *dQ = static_cast<In *>(A.dQ), *dK = static_cast<In *>(A.dK);
     if (n > 0)
         for (int r = tid % 128; r < d; r += 128) {
-            float a1[16], a2[16], a3[16];
+            float a1[kGRows], a2[kGRows], a3[kGRows];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) a1[i] = a2[i] = a3[i] = 0.f;
+            for (int i = 0; i < kGRows; ++i) a1[i] = a2[i] = a3[i] = 0.f;
             for (int e = 0; e < dv; e += 4) {
                 float s0[4], ds[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     s0[j] = e + j < dv ? S0[(size_t)r * dv + e + j] : 0.f;
                     ds[j] = e + j < dv ? R[(size_t)r * dv + e + j] : 0.f;
-                    if (half == 0) in = fmaf(s0[j], ds[j], in);
+                    if (group == 0) in = fmaf(s0[j], ds[j], in);
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < kGRows; ++i) {
                     const float4 o = *reinterpret_cast<const float4 *>(dO + (i0 + i) * pv + e);
                     const float4 y = *reinterpret_cast<const float4 *>(x + (i0 + i) * pv + e);
                     const float4 z = *reinterpret_cast<const float4 *>(u + (i0 + i) * pv + e);
@@ -576,7 +585,7 @@ __global__ void __launch_bounds__(kGThreads) delta_rec_grads_kernel(const GradAr
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < kGRows; ++i) {
                 const int t = i0 + i;
                 a1[i] *= p.scale * e0[t];
                 a2[i] *= e0[t];
@@ -615,7 +624,7 @@ __global__ void __launch_bounds__(kGThreads) delta_rec_grads_kernel(const GradAr
             }
         }
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < kGRows; ++i)
         for (int o = 16; o; o >>= 1) {
             acc_row[i] += __shfl_xor_sync(~0u, acc_row[i], o);
             acc_key[i] += __shfl_xor_sync(~0u, acc_key[i], o);
@@ -623,20 +632,20 @@ __global__ void __launch_bounds__(kGThreads) delta_rec_grads_kernel(const GradAr
     for (int o = 16; o; o >>= 1) in += __shfl_xor_sync(~0u, in, o);
     if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            red[(warp * 16 + i) * 2] = acc_row[i];
-            red[(warp * 16 + i) * 2 + 1] = acc_key[i];
+        for (int i = 0; i < kGRows; ++i) {
+            red[(warp * kGRows + i) * 2] = acc_row[i];
+            red[(warp * kGRows + i) * 2 + 1] = acc_key[i];
         }
         inner[warp] = in;
     }
     __syncthreads();
     if (tid < C) {
         // running sums over the rows in fp64: 32 values, and the sums before and after t may cancel
-        const int w0 = (tid / 16) * 4, i = tid % 16;
+        const int w0 = (tid / kGRows) * 4, i = tid % kGRows;
         double ar = (double)rowM[tid] - (double)colM[tid], ak = 0.0, tot = 0.0;
         for (int w = 0; w < 4; ++w) {
-            ar += red[((w0 + w) * 16 + i) * 2];
-            ak += red[((w0 + w) * 16 + i) * 2 + 1];
+            ar += red[((w0 + w) * kGRows + i) * 2];
+            ak += red[((w0 + w) * kGRows + i) * 2 + 1];
             tot += inner[w];
         }
         double after = ar, before = ak;

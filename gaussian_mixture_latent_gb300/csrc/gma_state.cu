@@ -4,9 +4,9 @@
 // start (the last may be shorter), and a group keeps one fp32 scale:
 //   scale = max |x| (1 / 127),   code = rint(x / scale) in [-127, 127],   read back as code * scale,
 // in fp32: the product with the rounded 1 / 127, and an IEEE division, so that the format says which code a value on a
-// border gets.  The error of a value is at most half a step, max |x| / 254, and three roundings.  Rounding to 8 bits is the purpose of the cache; the recurrences themselves
-// keep their states in fp32.  In a [K, dv + 1] mixture memory whose dv is a multiple of 32 the normaliser column is a
-// group of its own and comes back to within one rounding.
+// border gets.  The error of a value is at most half a step, max |x| / 254, and three roundings.  Rounding to 8 bits is
+// the purpose of the cache; the recurrences themselves keep their states in fp32.  In a [K, dv + 1] mixture memory whose
+// dv is a multiple of 32 the normaliser column is a group of its own and comes back to within three roundings.
 //
 // Bound by memory: 5.125 bytes an element (at cols a multiple of 32).  A thread takes four neighbouring elements (one
 // float4, one char4), eight threads a group, and kUnroll such pieces at a time so that enough loads are in flight.
