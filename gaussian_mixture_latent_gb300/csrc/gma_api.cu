@@ -604,7 +604,7 @@ const char *gma_status_string(gma_status status) {
         case GMA_ERR_WORKSPACE: return "GMA_ERR_WORKSPACE: workspace missing or too small";
         case GMA_ERR_CUDA: return "GMA_ERR_CUDA: CUDA runtime error or failed launch";
         case GMA_ERR_TIMEOUT: return "GMA_ERR_TIMEOUT: a device-side bounded wait ran out";
-        case GMA_ERR_BOUNDS: return "GMA_ERR_BOUNDS: a device-side index check failed (debug build)";
+        case GMA_ERR_BOUNDS: return "GMA_ERR_BOUNDS: a device-side index check failed";
     }
     return "unknown gma_status";
 }

@@ -5,12 +5,14 @@ Per batch entry and value head (key head h // (H // Hk)), with a float32 state S
 
 The functions check and marshal torch tensors; the computation is in the library's kernels.  Tensors are on
 one CUDA device, which is made current for the call; the call runs on `stream`, or on that device's current
-stream.  Scratch memory: `workspace` (uint8, of the size that the library asks for, its first 256 bytes zero),
-or a buffer kept per device and stream; while a CUDA graph is captured, a buffer of the graph's own.
+stream.  They are contiguous and start on 16 bytes.  Scratch memory: `workspace` (uint8, of the size that the
+library asks for, its first 256 bytes zero; for one call at a time), or a buffer kept per device and stream,
+which host threads may share; while a CUDA graph is captured, a buffer of the graph's own.
 """
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -52,9 +54,18 @@ def _lib():
 
 _FLOATS = (torch.float32, torch.bfloat16)
 _scratch: dict = {}
+# held while a call's kernels are launched: those of two host threads on one stream share a scratch buffer, and one
+# call's kernels must not come between the other's
+_launching = threading.RLock()
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream       # the current stream's handle without a Stream object
+
+
+def _sizes(what, *sizes):
+    """Sizes that do not fit the C interface's ints (ctypes would cut them) are refused."""
+    if max(sizes) > 0x7fffffff:
+        raise _gma.GmaError(2, what)
 
 
 def _check(t, name, shape, dtypes, index):
@@ -106,24 +117,31 @@ class _Call:
     def _run(self, fn, need, args, check_status):
         ws = self.workspace
         if ws is None:
-            # a buffer of this device and stream; a graph that is being captured gets one of its own
-            capturing = torch.cuda.is_current_stream_capturing()
-            ws = None if capturing else _scratch.get((self.index, self.ptr))
-            if ws is None or ws.numel() < need:
-                # allocated on the call's own stream, so that a buffer that is replaced is reused in its order
-                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=_device(self.index))
-                _gma.gma_workspace_init(ws)
-                if not capturing:
-                    _scratch[(self.index, self.ptr)] = ws
-        elif (ws.get_device() != self.index or ws.dtype != torch.uint8 or not ws.is_contiguous()):
-            raise ValueError(f"{self.what}: workspace must be a contiguous uint8 tensor on cuda:{self.index}")
-        elif ws.numel() < need:
-            raise _gma.GmaError(3, self.what)
-        rc = fn(*args, ws.data_ptr(), ws.numel(), self.ptr)
+            with _launching:
+                ws = self._own(need)
+                rc = fn(*args, ws.data_ptr(), ws.numel(), self.ptr)
+        else:
+            if ws.get_device() != self.index or ws.dtype != torch.uint8 or not ws.is_contiguous():
+                raise ValueError(f"{self.what}: workspace must be a contiguous uint8 tensor on cuda:{self.index}")
+            if ws.numel() < need:
+                raise _gma.GmaError(3, self.what)
+            rc = fn(*args, ws.data_ptr(), ws.numel(), self.ptr)
         if rc:
             raise _gma.GmaError(rc, self.what)
         if check_status:
             _gma._check_device_status(ws, self.stream, self.what)
+
+    def _own(self, need):
+        """The buffer of this device and stream; a graph that is being captured gets one of its own."""
+        capturing = torch.cuda.is_current_stream_capturing()
+        ws = None if capturing else _scratch.get((self.index, self.ptr))
+        if ws is None or ws.numel() < need:
+            # allocated on the call's own stream, so that a buffer that is replaced is reused in its order
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=_device(self.index))
+            _gma.gma_workspace_init(ws)
+            if not capturing:
+                _scratch[(self.index, self.ptr)] = ws
+        return ws
 
 
 _devices: dict = {}
@@ -164,11 +182,12 @@ def _sequence(what, size, Qx, Kx, V, g, beta, lengths, scale, stream, workspace)
         raise ValueError(f"V has {H} heads, expected a multiple of Qx's {Hk}")
     if lengths is not None:
         _check(lengths, "lengths", (B,), (torch.int32,), dev)
+    scale = d ** -0.5 if scale is None else float(scale)       # a number: of a tensor, its value at this call
     key = (size, B, H, Hk, N, d, dv, dt, gt, scale)
     plan = _plans.get(key)
     if plan is None:
-        desc = gma_delta_desc(B, H, Hk, N, d, dv, _gma._DTYPES[dt], _gma._DTYPES[gt],
-                              d ** -0.5 if scale is None else float(scale))
+        _sizes(what, B, H, Hk, N, d, dv)
+        desc = gma_delta_desc(B, H, Hk, N, d, dv, _gma._DTYPES[dt], _gma._DTYPES[gt], scale)
         n = ctypes.c_size_t(0)
         rc = getattr(_lib(), size)(ctypes.byref(desc), ctypes.byref(n))
         if rc:
@@ -283,6 +302,7 @@ def _cache(what, state, codes, scales, src, dst, stream, workspace):
     for name, t in (("src", src), ("dst", dst)):
         if t is not None:
             _check(t, name, (n,), (torch.int32,), dev)
+    _sizes(what, n, S, P, H * R, cols)
     return gma_state_desc(n, S, P, H * R, cols), call
 
 

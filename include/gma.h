@@ -351,9 +351,9 @@ gma_status gma_project(const gma_proj_desc *desc, const void *X, const void *Wq,
  *     not exist: their inputs are not used, out and every gradient is 0 there.
  * d, dv from 1 to 256; H a multiple of Hk.  g is a log decay, normally <= 0;
  * minus infinity or any value whose e^g is 0 in float32 (below about -104)
- * forgets the state (a document boundary).  The recurrence is stable while beta |Kx|^2 <= 2.  beta = 0 with
- * g = 0 leaves the state as it is.  A NaN or an infinity in a row may reach
- * rows of the same 64-row chunk before it.
+ * forgets the state (a document boundary).  The recurrence is stable while
+ * beta |Kx|^2 <= 2.  beta = 0 with g = 0 leaves the state as it is.  A NaN or an
+ * infinity in a row may reach rows of the same 64-row chunk before it.
  */
 typedef struct {
     int B, H, Hk, N, d, dv;
@@ -405,9 +405,9 @@ gma_status gma_delta_decode(const gma_delta_desc *desc, const void *Qx, const vo
  * Each row is cut into groups of 32 from its start, the last one maybe shorter:
  *   scale = max |x| (1 / 127),  code = rint(x / scale)
  * (float32: a product with the rounded 1 / 127, an IEEE division)
- * and reads back as code * scale; the error is at most max |x| / 254 and
- * three roundings.  A group
- * that holds a NaN or an infinity reads back as NaN.
+ * and reads back as code * scale; the error is at most max |x| / 254 and three
+ * roundings.  A group that holds a NaN or an infinity reads back as NaN.
+ * Contiguous, 16-byte aligned:
  *   state  [n_states, rows, cols] float32     codes [n_cache, rows, cols] int8
  *   scales [n_cache, rows, ceil(cols / 32)] float32
  *   src, dst [n] int32 or NULL (entry i at i): where each state is read and
@@ -458,7 +458,8 @@ gma_status gma_forward_noalloc(const gma_desc *desc, const void *Qx, const void 
  * Synchronises `stream`, reads the device status word of `workspace`, clears
  * it, and returns GMA_OK or the device error that was posted: GMA_ERR_TIMEOUT,
  * or GMA_ERR_BOUNDS from gma_delta_decode(), gma_state_store() or
- * gma_state_load() for an index outside its pool, or from a library built with GMA_DEBUG_BOUNDS defined, whose
+ * gma_state_load() for an index outside its pool, or from a library built with
+ * GMA_DEBUG_BOUNDS defined, whose
  * kernels check their global-memory indices (partial slots, heads, rows,
  * tiles) against the problem and skip, rather than perform, an access that
  * fails (a timeout is reported first when both were posted).

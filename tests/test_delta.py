@@ -176,6 +176,14 @@ def test_refusals_through_the_c_interface():
     assert dec(ws=None) == 3 and dec(wsb=255) == 3 and dec(d=desc(N=0)) == 0 and dec(d=desc(d=300)) == 2
 
 
+def test_sizes_beyond_the_c_interface_are_refused():
+    from gaussian_mixture_latent_gb300 import GmaError, delta
+    delta._sizes("x", 1, 2 ** 31 - 1)
+    with pytest.raises(GmaError) as e:
+        delta._sizes("x", 1, 2 ** 32 + 8)
+    assert e.value.code == 2
+
+
 @pytest.mark.parametrize("what", ["forward", "backward", "decode"])
 def test_python_refusals_on_cpu_tensors(what):
     import gaussian_mixture_latent_gb300 as m
@@ -514,6 +522,41 @@ def test_python_refusals(gma):
 
 
 # ------------------------------------------------------------------------------------------ GPU: streams and graphs
+
+@gpu
+def test_two_host_threads_on_one_stream(gma):
+    """Calls of several kernels each, from two threads, share the stream's scratch buffer: neither sees the other's."""
+    import threading
+    xs = [cuda(make(1, 4, n, 64, 64, "bf16", seed=n)) for n in (200, 330)]
+    call = lambda x: gma.gma_delta_backward(*(x[n] for n in ARGS), x["dO"])[:5]
+    want = [call(x) for x in xs]
+    torch.cuda.synchronize()
+    wrong, stream = [], torch.cuda.current_stream()
+
+    def work(i):
+        with torch.cuda.stream(stream):
+            got = [call(xs[i]) for _ in range(200)]
+            torch.cuda.synchronize()
+            wrong.append(sum(not all(torch.equal(a, b) for a, b in zip(g, want[i])) for g in got))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0, 0]
+
+
+@gpu
+def test_scale_given_as_a_tensor_is_read_at_each_call(gma):
+    x = cuda(make(1, 2, 40, 64, 64, "bf16"))
+    a = [x[n] for n in ARGS]
+    scale = torch.tensor(0.5)
+    first = gma.gma_delta_forward(*a, scale=scale)
+    assert torch.equal(first, gma.gma_delta_forward(*a, scale=0.5))
+    scale.fill_(0.25)                                    # half of it: a power of two, so that every rounding halves too
+    assert torch.equal(gma.gma_delta_forward(*a, scale=scale), first / 2)
+
 
 @gpu
 def test_two_streams_at_once(gma):
