@@ -98,9 +98,9 @@ __device__ __forceinline__ uint32_t at(int r, int c) {
     return r * ROWB + ((c ^ ((r / per) & mask)) << 4);
 }
 
-// 64 rows of a bf16 matrix (rows of `stride` elements at src) into a tile of ROWB-byte rows, by THREADS threads: zeros in the
-// rows from `rows` and the columns from `cols` on.  A thread stays in one piece column and steps by whole groups of eight
-// rows, so that its place in the tile is computed once.
+// 64 rows of a bf16 matrix (rows of `stride` elements at src) into a tile of ROWB-byte rows, by THREADS threads: zeros in
+// the rows from `rows` and the columns from `cols` on.  A thread stays in one piece column and steps by whole groups of
+// eight rows, so that its place in the tile is computed once.
 template <int ROWB, int THREADS>
 __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16 *src, int stride, int rows, int cols, int tid) {
     constexpr int kPieces = ROWB / 16, kStep = THREADS / kPieces;

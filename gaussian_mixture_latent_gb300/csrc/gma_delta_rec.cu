@@ -439,6 +439,8 @@ cudaError_t seqs_dispatch(const DeltaProblem &pb, const DeltaRec &back, const De
 //          + e^{G_C} <S0, R>,   M_ij = D_ij (scale (dO_i.u_j)(q_i.k_j) - (x_i.u_j)(k_i.k_j))
 // The first sum is taken as running sums of (row sums - column sums) of M over the rows i, j; pairs with both rows
 // on one side of t then cancel as the same numbers in fp32.
+// Latency-bound, one CTA to an SM at the usual sizes: 512 threads take 68 us for 8 heads x 515 rows of 64 x 128, 256
+// threads 76.
 constexpr int kGThreads = 512;
 constexpr int C = kRecChunk;
 constexpr int kGRows = C * 128 / kGThreads;           // rows of the chunk to each of the groups of 128 threads

@@ -28,8 +28,8 @@ constexpr int C = kTcRows;
 // One CTA of eight warps to a chunk.  Warps 0-3 take a row block of K K^T each and the inverse, warps 4-7 Q K^T.
 // T is inverted in fp32: 16 x 16 diagonal blocks by substitution (a product of powers would overflow for repeated
 // keys), joined to 32 and 64 by X21 = -T22 (A21 T11) with products of NT terms.  Bound by issue slots and the latency of
-// that chain of small steps: three or four CTAs share an SM (148 us for the 12288 chunks of 96 heads x 8192 rows of 64 x 64,
-// 3.2 TB/s; 58 % of the issue slots; two CTAs an SM took 210 us).
+// that chain of small steps: three or four CTAs share an SM (146 us for the 12288 chunks of 96 heads x 8192 rows of
+// 64 x 64, 3.2 TB/s; 62 % of the issue slots; two CTAs an SM took 210 us).
 constexpr int kPrepThreads = 256;
 enum { kBarInv = 1, kBarPair = 2 };    // named barriers; the pairs use 2..5
 
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kern
     char *P = to_ws + W::oP;
     const int ar = (lane & 7) + ((lane >> 3) & 1) * 8, ac = lane >> 4;      // A operand: row, 16-byte piece
     const int br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;      // B operand of two n tiles
-                // rows 16 rb.. of K K^T (Q K^T), up to the diagonal
+    // rows 16 rb.. of K K^T (Q K^T), up to the diagonal
     float x[8][4];
 #pragma unroll
     for (int n = 0; n < 8; ++n)
@@ -272,21 +272,21 @@ __global__ void __launch_bounds__(kPrepThreads, D == 64 ? 4 : 3) delta_prep_kern
 // same work under the triangles), then the columns of S^T; in between they exchange partial sums, R and U through shared
 // memory, lane by lane.
 // As many helper warps to a slice take what the next chunk does not wait for, each for the same tiles of eight rows (or its
-// part of d).  kFwd: O, from the state (one bf16 term) and U
-// that the chain leaves in shared memory.  kCkpt and kBack: the stores; kBack also the products of dO with P and Q, which
-// the chain adds.  Four loader warps copy chunk c + kStages - 1 while chunk c is worked on.
+// part of d).  kFwd: O, from the state (one bf16 term) and U that the chain leaves in shared memory.  kCkpt and kBack:
+// the stores; kBack also the products of dO with P and Q, which the chain adds.  Four loader warps copy chunk
+// c + kStages - 1 while chunk c is worked on.
 //
-// kCkpt (for the backward): no O; writes S before each chunk (two bf16 terms, [dv, d]) and W = U / beta, with |beta| held to at
-// least 2^-64 (a beta of 0 then adds 2^-64 W to the state, nothing in fp32).
+// kCkpt (for the backward): no O; writes S before each chunk (two bf16 terms, [dv, d]) and W = U / beta, with |beta| held
+// to at least 2^-64 (a beta of 0 then adds 2^-64 W to the state, nothing in fp32).
 // kBack: the reverse recurrence, with the state R = dL/dS [d, dv] after the chunk:
 //   dU = P^T dO + diag(f) K R,  X = T^T dU,  R <- e^{G_C} R + (scale diag(e^G) Q)^T dO - (diag(e^G beta) K)^T X,
 // the same chain with the triangles transposed; writes R after each chunk (bf16) and X.
 //
 // Bound by the chain: mma.sync issues one m16n8k16 each 8.0 cycles on each of the SM's four tensor units (measured,
 // 1 to 16 warps; latency 21), and the products of a chunk depend on one another.  64 x 64, SL = 4: 280 products of 8
-// cycles on each unit, 2240 of the 4000 cycles that a chunk takes (269 us for 96 heads x 8192 rows).  tcgen05 has four times that rate,
-// but its accumulators are in TMEM: three dependent products a chunk would each pay a round trip (load, split, store,
-// fence, issue) of about a chunk's time here.
+// cycles on each unit, 2240 of the 4000 cycles that a chunk takes (272 us for 96 heads x 8192 rows).  tcgen05 has four
+// times that rate, but its accumulators are in TMEM: three dependent products a chunk would each pay a round trip (load,
+// split, store, fence, issue) of about a chunk's time here.
 enum Mode { kFwd, kCkpt, kBack };
 constexpr int kGroup = 128;            // threads of the chain, of the helpers, of the loaders
 // Registers: launched with 168 a thread, 3 x 128 x 168 = 64512 = 128 x (240 + 192 + 72).
@@ -309,8 +309,10 @@ struct ChainSmem {
     static constexpr int KS = 4 / SL;
     static constexpr int kRow = 2 * D, kKey = C * kRow, kValRow = 32 * SL, kVal = C * kValRow;
     static constexpr int oQ = kKey, oV = 2 * kKey, oW = oV + kVal, kStage = oW + Chunk<NT>::bytes;
-    // of one slice: partial sums; R's terms, then U (float4 [8 tiles][32 lanes]); the state in kHeld bf16 terms; kBack: P^T dO and Q^T dO
-    static constexpr int kSum = KS > 1 ? KS * 4096 : 0, kRows = KS > 1 && NT > 2 ? 6144 : 4096, kHeld = MODE == kCkpt ? 2 : 1, kState = kHeld * 32 * D;
+    // of one slice: partial sums; R's terms, then U (float4 [8 tiles][32 lanes]); the state in kHeld bf16 terms; kBack:
+    // P^T dO and Q^T dO
+    static constexpr int kSum = KS > 1 ? KS * 4096 : 0, kRows = KS > 1 && NT > 2 ? 6144 : 4096;
+    static constexpr int kHeld = MODE == kCkpt ? 2 : 1, kState = kHeld * 32 * D;
     static constexpr int kZ = MODE == kBack ? 4096 + 64 * D : 0;
     static constexpr int oRows = kSum, oState = oRows + kRows, oZ = oState + kState, kSlice = oZ + kZ;
     static constexpr int kStages = 3 * kStage + SL * kSlice <= 227 * 1024 ? 3 : 2;
@@ -782,7 +784,9 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
     chain_cta<D, NT, SL, kFwd>(a, blockIdx.x);
 }
 
-// The two chains of the backward, which do not depend on one another: the reverse one, which takes longer, first.
+// The two chains of the backward, which do not depend on one another: the reverse one, which takes longer, first.  With
+// fewer CTAs in each than SMs they run side by side (96 heads x 8192 rows of 64 x 64: 560 us, one after the other
+// 279 + 343; 2 x 8 heads x 1999 rows of 128 x 128: 82 us, 52 + 56).
 template <int D, int NT, int SL>
 __global__ void __launch_bounds__(3 * kGroup, 1) delta_chains_kernel(const ChainArgs back, const ChainArgs ckpt) {
     const int n = gridDim.x / 2;

@@ -10,8 +10,8 @@
 //
 // Bound by memory: 5.125 bytes an element (at cols a multiple of 32).  A thread takes four neighbouring elements (one
 // float4, one char4), eight threads a group, and kUnroll such pieces at a time so that enough loads are in flight.
-// Measured, 96 states of 32 x 128 x 128: store 63 us (258 MB, 4.1 TB/s; bound by issue: a group's maximum, its two divisions
-// and four roundings for each 20 bytes a thread moves), load 39 us (6.6 TB/s).
+// Measured, 96 states of 32 x 128 x 128: store 62 us (258 MB, 4.1 TB/s; bound by issue, 71 % of its slots: a group's
+// maximum, its divisions and four roundings for each 20 bytes a thread moves), load 39 us (6.6 TB/s).
 #include <cstdint>
 
 #include "gma_delta.h"
