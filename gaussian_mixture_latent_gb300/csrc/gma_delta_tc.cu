@@ -442,7 +442,9 @@ __device__ __forceinline__ void chain_cta(const ChainArgs &a, const int block) {
                 if (MODE != kCkpt) load_tile<L::kRow, kGroup>(st + L::oQ, Q + (krow + c * C) * p.d, p.d, len - c * C, p.d, lt);
                 load_tile<L::kValRow, kGroup>(st + L::oV, V + (vrow + c * C) * p.dv + c0, p.dv, len - c * C, p.dv - c0, lt);
                 const char *ws = a.chunks + ((size_t)bh * a.nc + c) * W::bytes;
-                for (int i = lt; i < W::bytes / 16; i += kGroup) copy16(st + L::oW + 16 * i, ws + 16 * i, true);
+                for (int i = lt; i < W::bytes / 16; i += kGroup)
+                    if (MODE != kCkpt || i < W::oP / 16 || i >= W::oVec / 16)         // no O, no P
+                        copy16(st + L::oW + 16 * i, ws + 16 * i, true);
             }
             copy_commit();
         };
