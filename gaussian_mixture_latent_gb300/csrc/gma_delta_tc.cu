@@ -787,8 +787,8 @@ __global__ void __launch_bounds__(3 * kGroup, 1) delta_chain_kernel(const ChainA
 }
 
 // The two chains of the backward, which do not depend on one another: the reverse one, which takes longer, first.  With
-// fewer CTAs in each than SMs they run side by side (96 heads x 8192 rows of 64 x 64: 560 us, one after the other
-// 279 + 343; 2 x 8 heads x 1999 rows of 128 x 128: 82 us, 52 + 56).
+// fewer CTAs in each than SMs they run side by side (96 heads x 8192 rows of 64 x 64: 560 us against 279 + 343 one after
+// the other, and 550 since kCkpt leaves P out; 2 x 8 heads x 1999 rows of 128 x 128: 82 us against 52 + 56).
 template <int D, int NT, int SL>
 __global__ void __launch_bounds__(3 * kGroup, 1) delta_chains_kernel(const ChainArgs back, const ChainArgs ckpt) {
     const int n = gridDim.x / 2;
