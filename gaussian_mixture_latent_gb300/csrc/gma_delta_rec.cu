@@ -670,8 +670,8 @@ __global__ void __launch_bounds__(kGThreads) delta_rec_grads_kernel(const GradAr
 }
 
 template <typename In>
-__global__ void __launch_bounds__(256) delta_sum_heads_kernel(const float *dq, const float *dk, In *dQ, In *dK, int Hk,
-                                                              int r, size_t head, size_t total) {
+__global__ void __launch_bounds__(256) delta_sum_heads_kernel(const float *dq, const float *dk, In *dQ, In *dK, int r,
+                                                              size_t head, size_t total) {
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
         const size_t bk = i / head, e = i % head;        // [B * Hk] key heads of `head` = N * d elements
         const size_t first = bk * r * head + e;
@@ -721,10 +721,9 @@ cudaError_t delta_sum_heads(const DeltaProblem &p, const float *dq, const float 
     const size_t head = (size_t)p.N * p.d, total = head * p.B * p.Hk;
     const unsigned grid = (unsigned)(total / 256 + 1 < 152 * 16 ? total / 256 + 1 : 152 * 16);
     if (p.bf16)
-        delta_sum_heads_kernel<<<grid, 256, 0, s>>>(dq, dk, (__nv_bfloat16 *)dQ, (__nv_bfloat16 *)dK, p.Hk, p.H / p.Hk,
-                                                    head, total);
+        delta_sum_heads_kernel<<<grid, 256, 0, s>>>(dq, dk, (__nv_bfloat16 *)dQ, (__nv_bfloat16 *)dK, p.H / p.Hk, head, total);
     else
-        delta_sum_heads_kernel<<<grid, 256, 0, s>>>(dq, dk, (float *)dQ, (float *)dK, p.Hk, p.H / p.Hk, head, total);
+        delta_sum_heads_kernel<<<grid, 256, 0, s>>>(dq, dk, (float *)dQ, (float *)dK, p.H / p.Hk, head, total);
     return cudaGetLastError();
 }
 

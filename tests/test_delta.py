@@ -521,6 +521,67 @@ def test_python_refusals(gma):
         gma.gma_delta_decode(*a, None)
 
 
+# ------------------------------------------------------------------------------------------ GPU: offsets past 32 bits
+
+@gpu
+def test_sequences_of_more_than_2_31_elements(gma):
+    """The last head of a call whose V has more than 2^31 elements, against that head in a call of its own.  The two
+    calls may share a head's columns over warps differently: each is within test_forward's and test_backward's bounds."""
+    H, N, d, dv = 264, 65536, 64, 128
+    assert H * N * dv > 2 ** 31
+    gen = torch.Generator("cuda").manual_seed(5)
+
+    def rand(last):
+        x = torch.empty((1, H, N, last), dtype=torch.bfloat16, device="cuda")
+        return x.normal_(generator=gen)
+
+    def keys():                                          # about unit length
+        return rand(d).mul_(d ** -0.5)
+
+    x = [keys(), keys().mul_(0.75), rand(dv), -0.2 * torch.rand((1, H, N), generator=gen, device="cuda"),
+         torch.rand((1, H, N), generator=gen, device="cuda")]
+    dO = rand(dv)
+    out = gma.gma_delta_forward(*x, check_status=True)[:, -1:].clone()
+    grads = [t[:, -1:].clone() for t in gma.gma_delta_backward(*x, dO, check_status=True)[:5]]
+    one = [t[:, -1:].clone() for t in x]
+    dO = dO[:, -1:].clone()
+    del x
+    near = lambda a, b, lim: float((a.float() - b.float()).abs().max()) <= lim * float(b.float().abs().max())
+    try:
+        assert near(out, gma.gma_delta_forward(*one), 6 * 2.0 ** -8)
+        for a, b in zip(grads, gma.gma_delta_backward(*one, dO)[:5]):
+            assert near(a, b, 8 * 2.0 ** -8)
+    finally:
+        from gaussian_mixture_latent_gb300 import delta
+        torch.cuda.synchronize()
+        delta._scratch.clear()                           # some tens of GB
+        torch.cuda.empty_cache()
+
+
+@gpu
+def test_pools_of_more_than_2_31_elements(gma):
+    S, H, d, dv = 2100, 64, 128, 128
+    assert (S - 2) * H * d * dv > 2 ** 31
+    x = cuda(make(2, H, 1, d, dv, "bf16", seed=8))
+    a = [x[n] for n in ARGS]
+    pool = torch.empty((S, H, d, dv), device="cuda")
+    codes = torch.empty((S, H, d, dv), dtype=torch.int8, device="cuda")
+    scales = torch.empty((S, H, d, dv // 32), device="cuda")
+    small = torch.randn((2, H, d, dv), device="cuda")
+    t = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    pool[S - 1], pool[3] = small[0], small[1]
+    out = gma.gma_delta_decode(*a, pool, slots=t(S - 1, 3), check_status=True)
+    assert torch.equal(out, gma.gma_delta_decode(*a, small))
+    assert torch.equal(pool[S - 1], small[0]) and torch.equal(pool[3], small[1])
+    gma.gma_state_store(pool, codes, scales, src=t(S - 1, 3), dst=t(S - 2, 1), check_status=True)
+    gma.gma_state_load(codes, scales, pool, src=t(S - 2, 1), dst=t(S - 2, 0), check_status=True)
+    c, s, back = torch.empty_like(codes[:2]), torch.empty_like(scales[:2]), torch.empty_like(small)
+    gma.gma_state_store(small, c, s)
+    gma.gma_state_load(c, s, back)
+    assert torch.equal(codes[S - 2], c[0]) and torch.equal(codes[1], c[1]) and torch.equal(scales[S - 2], s[0])
+    assert torch.equal(pool[S - 2], back[0]) and torch.equal(pool[0], back[1])
+
+
 # ------------------------------------------------------------------------------------------ GPU: streams and graphs
 
 @gpu
