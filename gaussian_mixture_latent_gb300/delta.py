@@ -68,6 +68,13 @@ def _sizes(what, *sizes):
         raise _gma.GmaError(2, what)
 
 
+def _dims(t, name, dims):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} has {t.dim()} dimensions, expected {dims}")
+
+
 def _check(t, name, shape, dtypes, index):
     """t is a contiguous CUDA tensor of this shape and of one of these types on device `index`."""
     if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.get_device() == index
@@ -106,6 +113,10 @@ class _Call:
         device, stream = self._there()
         with device, stream:
             return torch.empty(shape, dtype=dtype, device=_device(self.index))
+
+    def like(self, t):
+        """New memory of t's shape and type."""
+        return torch.empty_like(t) if self.here else self.empty(t.shape, t.dtype)
 
     def run(self, fn, need, args, check_status):
         if self.here:
@@ -163,21 +174,23 @@ _plans: dict = {}
 
 def _sequence(what, size, Qx, Kx, V, g, beta, lengths, scale, stream, workspace):
     """The checked description, workspace size and call of one gated-delta-rule problem."""
-    for name, t, dims in (("Qx", Qx, 4), ("V", V, 4), ("g", g, 3)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dim() != dims:
-            raise ValueError(f"{name} has {t.dim()} dimensions, expected {dims}")
-    B, Hk, N, d = keys = Qx.shape
-    _, H, _, dv = V.shape
+    try:
+        B, Hk, N, d = keys = Qx.shape
+        _, H, _, dv = V.shape
+        _, _, _ = g.shape
+    except (AttributeError, ValueError):
+        for name, t, dims in (("Qx", Qx, 4), ("V", V, 4), ("g", g, 3)):
+            _dims(t, name, dims)
+        raise
     dt, gt = Qx.dtype, g.dtype
     call = _Call(what, Qx, stream, workspace)
     dev = call.index
     _check(Qx, "Qx", keys, _FLOATS, dev)
     _check(Kx, "Kx", keys, (dt,), dev)
-    _check(V, "V", (B, H, N, dv), (dt,), dev)
-    _check(g, "g", (B, H, N), _FLOATS, dev)
-    _check(beta, "beta", (B, H, N), (gt,), dev)
+    rows = (B, H, N)
+    _check(V, "V", rows + (dv,), (dt,), dev)
+    _check(g, "g", rows, _FLOATS, dev)
+    _check(beta, "beta", rows, (gt,), dev)
     if Hk == 0 or H % Hk:
         raise ValueError(f"V has {H} heads, expected a multiple of Qx's {Hk}")
     if lengths is not None:
@@ -211,7 +224,7 @@ def gma_delta_forward(Qx, Kx, V, g, beta, state=None, lengths=None, scale=None, 
                                  stream, workspace)
     shape = (V.shape[0], V.shape[1], Qx.shape[3], V.shape[3])
     if out is None:
-        out = call.empty(V.shape, V.dtype)
+        out = call.like(V)
     else:
         _check(out, "out", V.shape, (V.dtype,), call.index)
     if state is not None:
@@ -243,7 +256,7 @@ def gma_delta_backward(Qx, Kx, V, g, beta, dO, state=None, dstate=None, lengths=
     if grads is not None and len(grads) != 6:
         raise ValueError(f"grads has {len(grads)} entries, expected 6")
     if grads is None:
-        grads = tuple(None if t is None else call.empty(t.shape, t.dtype) for t in inputs)
+        grads = tuple(None if t is None else call.like(t) for t in inputs)
     else:
         for t, like, name in zip(grads, inputs, ("dQx", "dKx", "dV", "dg", "dbeta", "dstate_in")):
             if like is not None:
@@ -264,16 +277,13 @@ def gma_delta_decode(Qx, Kx, V, g, beta, state, slots=None, lengths=None, scale=
     (raised with check_status).  Returns out [B,H,N,dv]."""
     desc, need, call = _sequence("gma_delta_decode", "gma_delta_decode_workspace_size", Qx, Kx, V, g, beta, lengths,
                                  scale, stream, workspace)
-    if not isinstance(state, torch.Tensor):
-        raise TypeError("state must be a torch.Tensor")
-    if state.dim() != 4:
-        raise ValueError(f"state has {state.dim()} dimensions, expected 4")
+    _dims(state, "state", 4)
     pool = state.shape[0]
     _check(state, "state", (pool, V.shape[1], Qx.shape[3], V.shape[3]), (torch.float32,), call.index)
     if slots is not None:
         _check(slots, "slots", (V.shape[0],), (torch.int32,), call.index)
     if out is None:
-        out = call.empty(V.shape, V.dtype)
+        out = call.like(V)
     else:
         _check(out, "out", V.shape, (V.dtype,), call.index)
     call.run(_lib().gma_delta_decode, need,
@@ -283,11 +293,8 @@ def gma_delta_decode(Qx, Kx, V, g, beta, state, slots=None, lengths=None, scale=
 
 
 def _cache(what, state, codes, scales, src, dst, stream, workspace):
-    for name, t in (("state", state), ("codes", codes)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dim() != 4:
-            raise ValueError(f"{name} has {t.dim()} dimensions, expected 4")
+    _dims(state, "state", 4)
+    _dims(codes, "codes", 4)
     call = _Call(what, state, stream, workspace)
     dev = call.index
     S, H, R, cols = state.shape
